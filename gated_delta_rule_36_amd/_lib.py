@@ -23,6 +23,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SPLIT_MIN_AVG_TOKENS = 1024  # "auto" takes the two-phase path only past this average length
 _Z = ctypes.c_size_t
+_I64 = ctypes.c_int64
+_F = ctypes.c_float
 
 
 class Gdn2Error(RuntimeError):
@@ -79,6 +81,19 @@ def lib():
         L.gdn2_block_prologue.restype = _I
         L.gdn2_block_epilogue.argtypes = [_P] * 4 + [ctypes.c_long, _I, _I, _P]
         L.gdn2_block_epilogue.restype = _I
+        L.gdn2_qk_norm_rope.argtypes = [_P] * 8 + [_I] * 5 + [_I64] * 2 + [_I, _F, _I, _I, _P]
+        L.gdn2_qk_norm_rope.restype = _I
+        L.gdn2_qk_norm_rope_bwd.argtypes = ([_P] * 12 + [_I] * 5 + [_I64] * 2 +
+                                            [_I, _F, _I, _I, _P, _Z, _P])
+        L.gdn2_qk_norm_rope_bwd.restype = _I
+        L.gdn2_qk_norm_rope_bwd_workspace_bytes.argtypes = [_I] * 5
+        L.gdn2_qk_norm_rope_bwd_workspace_bytes.restype = _Z
+        L.gdn2_attn_prologue.argtypes = [_P] * 14 + [_I] * 8 + [_I64] * 3 + [_I, _F, _I, _I, _P]
+        L.gdn2_attn_prologue.restype = _I
+        L.gdn2_cache_attention.argtypes = [_P] * 9 + [_I] * 9 + [_F, _I, _P, _Z, _P]
+        L.gdn2_cache_attention.restype = _I
+        L.gdn2_cache_attention_workspace_bytes.argtypes = [_I] * 9
+        L.gdn2_cache_attention_workspace_bytes.restype = _Z
         L.gdn2_status_string.argtypes = [_I]
         L.gdn2_status_string.restype = ctypes.c_char_p
         L.gdn2_version.argtypes = []

@@ -365,6 +365,128 @@ int gdn2_block_prologue(const void* xq, const void* xk, const void* xv, const vo
 int gdn2_block_epilogue(const void* o, const void* gate, const float* weight, void* y,
                         long rows, int d_v, int dtype, void* hip_stream);
 
+/*
+ * The softmax-attention layer that a hybrid stack places beside the mixer (the reading note's
+ * §3 architecture paragraph: mixer, then sliding-window attention): per-head norms of queries
+ * and keys with the position rotation, for training; the same pass for serving, which also
+ * writes keys and values into a paged 8-bit cache; and attention over that cache.
+ */
+
+/* Flags of the norm-and-rotation entry points. */
+enum {
+  GDN2_ROPE_INTERLEAVED = 1, /* pairs (2i, 2i + 1) instead of (i, i + rot / 2) */
+  GDN2_ROPE_NO_NORM = 2      /* rotation only: no mean square; the weights still apply */
+};
+
+/*
+ * Norm of every head row of q and k and the position rotation, in one pass:
+ *     n = x / sqrt(mean(x^2) + eps) * weight
+ *     pair i < rot / 2, angle = position * inv_freq[i]:
+ *       y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin;   channels past rot: y = n
+ * fp32 throughout, the angle reduced in fp64 (exact for any int32 position), one rounding.
+ *
+ *   q, k               : [B, T, Hq, d], [B, T, Hk, d] (dtype). The rows of one token are dense;
+ *                        token t (of B * T) starts at element t * q_stride / t * k_stride, so
+ *                        q and k may be slices of one projection. Strides are at least H * d
+ *                        and multiples of 8.
+ *   q_weight, k_weight : [d] fp32, or NULL for ones
+ *   positions          : device int32 [B, T], or NULL for 0 .. T - 1 in every sequence
+ *   inv_freq           : device fp32 [rot / 2], radians per position (NULL when rot = 0)
+ *   rot                : rotated channels, a multiple of 8 in [0, d]
+ *   q_out, k_out       : dense [B, T, H, d] (dtype), written; may be q and k themselves where
+ *                        those are dense
+ *   Supported: d in {64, 128}, both dtypes. B * T = 0 is a no-op.
+ * Returns GDN2_OK or an error status.
+ */
+int gdn2_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                      const int32_t* positions, const float* inv_freq, void* q_out, void* k_out,
+                      int B, int T, int Hq, int Hk, int d, int64_t q_stride, int64_t k_stride,
+                      int rot, float eps, int flags, int dtype, void* hip_stream);
+
+/*
+ * Gradients of gdn2_qk_norm_rope: dq, dk (dense, dtype) from the dense gradients dq_out, dk_out
+ * of its outputs and its inputs, and the weights' gradients [d] fp32 (each NULL where not
+ * wanted; written also where the weight itself is NULL). dq may be dq_out, dk may be dk_out.
+ * The sums over rows are formed in a fixed order: equal inputs give equal bits.
+ *   workspace : needed where a weight gradient is: at least
+ *               gdn2_qk_norm_rope_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * B * T = 0 is a no-op (weight gradients are not written). Returns GDN2_OK or an error status.
+ */
+int gdn2_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                          const float* q_weight, const float* k_weight, const int32_t* positions,
+                          const float* inv_freq, void* dq, void* dk, float* dq_weight,
+                          float* dk_weight, int B, int T, int Hq, int Hk, int d, int64_t q_stride,
+                          int64_t k_stride, int rot, float eps, int flags, int dtype,
+                          void* workspace, size_t workspace_bytes, void* hip_stream);
+size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d);
+
+/*
+ * The 8-bit cache. Blocks of GDN2_CACHE_BLOCK tokens; per block and kv head one scale for the
+ * keys and one for the values, a power of two s; the value held is e4m3 (OCP e4m3fn) * s.
+ *   k_cache : [P, Hk, 64, d]  bytes, a key row per token
+ *   v_cache : [P, Hk, d, 64]  bytes, a row per channel; token t of the block is column
+ *             (t / 4 % 4) * 16 + (t / 16) * 4 + t % 4
+ *   k_scale, v_scale : [P, Hk] fp32
+ *   block_table : device int32 [N, max_blocks]: block b of sequence n holds its positions
+ *             64 b .. 64 b + 63. An entry outside [0, P), or a position past the table, is a
+ *             place that does not exist: nothing is written there and nothing is read.
+ *   seq_lens : device int32 [N]: tokens of every sequence, those of this call included. The
+ *             new tokens of a sequence are its last ones; where it has fewer tokens than new
+ *             rows, the leading rows hold no token (padding).
+ * The new rows come as a fixed number T per sequence ([N, T, H, d]: cu_seqlens NULL, N = B) or
+ * packed (cu_seqlens as for gdn2_chunk_fwd, B = 1).
+ */
+enum { GDN2_CACHE_BLOCK = 64 };
+
+/*
+ * Serving prologue of the attention layer: gdn2_qk_norm_rope on the new rows (position = place
+ * in the sequence), queries to q_out, keys and values into the cache.
+ *   A block's scale is the smallest power of two s >= 2^-64 with max|x| <= 448 s over the new
+ *   rows in it, and not below its scale so far unless the block's first position is among the
+ *   new rows (then what the block held is dropped: its value positions without a token are
+ *   cleared). Where a scale grows, the block's older codes are rescaled (exact, but for codes
+ *   that fall below e4m3's normal range).
+ *   A token whose key or value row holds a NaN or infinity (after norm and rotation) has a
+ *   key row of NaN and a zero value row in the cache and does not count for the scales: every
+ *   query of that head which attends to it comes out NaN, others are not touched.
+ *   q, k, v : rows as in gdn2_qk_norm_rope, strides of their own
+ *   q_out   : dense [.., Hq, d]; zeros in rows without a token; may be q where that is dense
+ *   Two sequences must not have a block in common that this call writes.
+ *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk. No tokens: a no-op.
+ * Returns GDN2_OK or an error status.
+ */
+int gdn2_attn_prologue(const void* q, const void* k, const void* v, const float* q_weight,
+                       const float* k_weight, const float* inv_freq, void* q_out, void* k_cache,
+                       void* v_cache, float* k_scale, float* v_scale, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* cu_seqlens, int B, int T, int Hq,
+                       int Hk, int d, int N, int P, int max_blocks, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, int rot, float eps, int flags,
+                       int dtype, void* hip_stream);
+
+/*
+ * Causal attention of the new rows over the cache, which already holds their own keys and
+ * values:  o_i = sum_j softmax_j(scale q_i . k_j) v_j,  j <= p_i, and j > p_i - window where
+ * window > 0. Query head h reads kv head h / (Hq / Hk). A row that sees no key (padding, an
+ * empty sequence, blocks that do not exist) is written as zeros; rows behind the last packed
+ * sequence are not written.
+ *   q, o      : dense [B, T, Hq, d] (dtype); o may be q
+ *   scale     : positive and finite, usually 1 / sqrt(d)
+ *   workspace : at least gdn2_cache_attention_workspace_bytes(...) bytes (0: may be NULL),
+ *               16-byte aligned, free for the call's duration on `hip_stream`. A captured call
+ *               uses it at every replay: two graphs that may run at once need one each.
+ *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk. No tokens: a no-op.
+ * Returns GDN2_OK or an error status.
+ */
+int gdn2_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* cu_seqlens, void* o, int B, int T,
+                         int Hq, int Hk, int d, int N, int P, int max_blocks, int window,
+                         float scale, int dtype, void* workspace, size_t workspace_bytes,
+                         void* hip_stream);
+/* packed: whether cu_seqlens is given; the other arguments as for the call. */
+size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, int Hk, int d, int N,
+                                            int max_blocks, int window);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char* gdn2_status_string(int status);
 

@@ -1,0 +1,472 @@
+"""GPU tests of the serving prologue and of attention over the 8-bit cache against the float64
+oracle, apart and as they are used together."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn2_attn as R
+from tests.attn_util import (B64, U, Paged, assert_within, attention_ref, draw, f64, half, inv_freq,
+                             rows_bound)
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _layout(new, packed, behind=0):
+    """Row spans of the new tokens, the leading shape and cu_seqlens."""
+    if packed:
+        cu = np.concatenate([[0], np.cumsum(new)])
+        return [(int(c), int(n)) for c, n in zip(cu, new)], (1, int(cu[-1]) + behind), _i32(cu)
+    assert len(set(new)) == 1
+    return [(i * new[0], new[0]) for i in range(len(new))], (len(new), new[0]), None
+
+
+# ---------------------------------------------------------------- prologue
+
+def _prologue(rng, paged, new, lens, Hq, packed, rot, il=False, norm=True, spoil=None, strided=True, behind=0,
+              sizes=1.0):
+    """One call on the device and in the oracle; checks q_out and the whole cache."""
+    import gated_delta_rule_36_amd as G
+    Hk, d = paged.Hk, paged.d
+    spans, lead, cu = _layout(new, packed, behind)
+    w = (Hq + 2 * Hk) * d
+    qkv = draw(rng, *lead, w + (8 if strided else 0), scale=sizes)
+    if spoil is not None:
+        spoil(qkv)
+    qkv = qkv.cuda()
+    q = qkv[..., : Hq * d].view(*lead, Hq, d)
+    k = qkv[..., Hq * d: (Hq + Hk) * d].view(*lead, Hk, d)
+    v = qkv[..., (Hq + Hk) * d: w].view(*lead, Hk, d)
+    wq, wk = (torch.from_numpy((1 + 0.2 * rng.standard_normal(d)).astype(np.float32)).cuda() for _ in range(2))
+    fr = inv_freq(rot)
+    out = torch.full((*lead, Hq, d), 7.0, dtype=BF, device="cuda")
+    before = paged.pull()
+    G.attn_prologue(q, k, v, paged.dev, paged.table_t(), _i32(lens), torch.from_numpy(fr).cuda() if rot else None,
+                    cu_seqlens=cu, q_weight=wq, k_weight=wk, interleaved=il, norm=norm, out=out)
+    torch.cuda.synchronize()
+    flat = {n: f64(t).reshape(-1, t.shape[2], d) for n, t in (("q", q), ("k", k), ("v", v))}
+    got = f64(out).reshape(-1, Hq, d)
+    ref, bound = np.full_like(got, 7.0), np.zeros_like(got)
+    errs = {}
+    for i, (first, n) in enumerate(spans):
+        if n == 0:
+            continue
+        pos = int(lens[i]) - n + np.arange(n)
+        rows = slice(first, first + n)
+        with np.errstate(invalid="ignore"):
+            y, b = rows_bound(flat["q"][rows], f64(wq), np.maximum(pos, 0), fr, BF, 1e-6, il, norm)
+            kn, kb = rows_bound(flat["k"][rows], f64(wk), np.maximum(pos, 0), fr, torch.float64, 1e-6, il, norm)
+        none = (pos < 0)[:, None, None]
+        ref[rows], bound[rows] = np.where(none, 0.0, y), np.where(none, 0.0, b)
+        R.append(paged.ref, paged.table[i], int(lens[i]), kn, flat["v"][rows])
+        errs[i] = kb
+    assert_within("q_out", got, ref, bound)
+    # scales are powers of two and equal; codes of the values are roundings of exact inputs and
+    # equal; a key's code may fall to the other side of a rounding border by fp32's error
+    # (16 U of the row), so it is at most one step off, and only where it is that near a border
+    k_, v_, ks_, vs_ = paged.pull()
+    assert np.array_equal(ks_, paged.ref.k_scale) and np.array_equal(vs_, paged.ref.v_scale)
+    wrong = np.argwhere(v_ != paged.ref.v)
+    assert len(wrong) == 0, wrong[:4]
+    assert np.array_equal(np.isnan(k_), np.isnan(paged.ref.k))
+    off = np.argwhere((k_ != paged.ref.k) & ~np.isnan(k_))
+    assert len(off) <= 1 + k_.size // 10000, len(off)
+    for at in off[:50]:
+        a, b = k_[tuple(at)], paged.ref.k[tuple(at)]
+        assert abs(a - b) <= 2 ** -3 * max(abs(a), abs(b)) + 2 ** -9, (at, a, b)
+    paged.ref.k[:] = k_  # the device's roundings from here on
+    return before, (k_, v_, ks_, vs_)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("total", [1, 2, 64, 65, 66, 100, 128, 129])
+def test_prologue_single_token(total, d):
+    """One token at every kind of place in a block, behind random older ones."""
+    rng = np.random.default_rng(total * 3 + d)
+    lens = [total, 70]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng)
+    say("attn_prologue one token", total, d)
+    _prologue(rng, paged, [1, 1], lens, 6, False, d, il=total % 2 == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens,packed", [
+    ([5] * 3, [5, 66, 200], False),
+    ([64] * 2, [64, 128], False),
+    ([70] * 2, [70, 133], False),
+    ([9] * 2, [60, 73], False),          # more tokens than go out as single bytes
+    ([3, 0, 150, 1, 64], [3, 0, 150, 90, 64], True),
+    ([1, 1, 1], [1, 64, 65], True),
+    ([130, 2], [131, 2], True),
+    ([300], [300], True),
+])
+def test_prologue_rows(new, lens, packed, d):
+    rng = np.random.default_rng(sum(new) + d)
+    paged = Paged(rng, lens, 3, d)
+    paged.fill(rng)
+    say("attn_prologue", new, lens, packed, d)
+    _prologue(rng, paged, new, lens, 3, packed, d // 2, behind=4 if packed else 0)
+
+
+def test_prologue_many_sequences_packed():
+    """More sequences than one round of the 64-way search, empty ones among them."""
+    rng = np.random.default_rng(5)
+    new = [int(x) for x in rng.integers(0, 4, 150)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 130, 150))]
+    paged = Paged(rng, lens, 1, 64)
+    paged.fill(rng)
+    say("attn_prologue 150 packed sequences")
+    _prologue(rng, paged, new, lens, 2, True, 64, behind=3)
+
+
+def test_prologue_scales_grow_and_shrink():
+    """Tokens of rising size into one block: the scale grows and older codes follow; a block
+    begun anew drops its old scale."""
+    rng = np.random.default_rng(6)
+    lens = [130]
+    paged = Paged(rng, lens, 2, 128)
+    say("attn_prologue growth")
+    scales = []
+    for t, size in ((3, 1e-3), (4, 1e-2), (6, 1.0), (7, 300.0), (9, 1e4), (30, 1.0), (64, 1.0)):
+        _prologue(rng, paged, [t - (paged.t if hasattr(paged, "t") else 0)], [t], 2, False, 128, norm=False, sizes=size)
+        paged.t = t
+        scales.append(paged.ref.k_scale[paged.table[0, 0], 0])
+    assert scales == sorted(scales) and scales[-1] > 1000 * scales[0]
+    _prologue(rng, paged, [2], [2], 2, False, 128, norm=False, sizes=1e-3)  # the block again, from its start
+    assert paged.ref.k_scale[paged.table[0, 0], 0] < 1e-4
+
+
+def test_prologue_padding_rows_and_missing_blocks():
+    rng = np.random.default_rng(7)
+    # more new rows than tokens; an empty sequence; a sequence past its table; a hole in a table
+    lens = [3, 0, 200, 130]
+    paged = Paged(rng, [3, 0, 200, 130], 2, 64, table_width=2)
+    paged.fill(rng)
+    paged.table[3, 1] = paged.P + 5
+    paged.table[2, 0] = -7
+    say("attn_prologue padding and missing blocks")
+    _prologue(rng, paged, [80] * 4, lens, 4, False, 64)
+
+
+def test_prologue_not_finite_tokens():
+    rng = np.random.default_rng(8)
+    lens = [70, 70]
+    Hq, Hk, d = 2, 2, 64
+    paged = Paged(rng, lens, Hk, d)
+
+    def spoil(x):
+        x[0, 5, (Hq + 1) * d + 3] = float("nan")           # key of head 1
+        x[0, 9, (Hq + Hk) * d + 1] = float("inf")          # value of head 0
+        x[1, 0, (Hq + Hk + 1) * d] = float("-inf")         # value of head 1
+        x[0, 68, Hq * d + 8] = float("inf")                # key of head 0, the last block
+
+    say("attn_prologue not finite")
+    _prologue(rng, paged, [70, 70], lens, Hq, False, d, norm=False, spoil=spoil)
+    assert np.isnan(paged.ref.k).any() and not np.isnan(paged.ref.v).any()
+
+
+def test_prologue_leaves_other_blocks():
+    rng = np.random.default_rng(9)
+    lens = [100, 300]
+    paged = Paged(rng, lens, 2, 128, spare=5)
+    paged.fill(rng)
+    say("attn_prologue other blocks")
+    before, after = _prologue(rng, paged, [3, 3], lens, 4, False, 128)
+    touched = {paged.table[0, 1], paged.table[1, 4]}
+    for b, a in zip(before, after):
+        for s in range(paged.P):
+            if s not in touched:
+                assert np.array_equal(b[s], a[s]), s
+
+
+# ---------------------------------------------------------------- attention
+
+def _attention(rng, paged, new, lens, Hq, packed=False, window=0, scale=None, behind=0, q=None, alias=False):
+    import gated_delta_rule_36_amd as G
+    spans, lead, cu = _layout(new, packed, behind)
+    q = draw(rng, *lead, Hq, paged.d) if q is None else q
+    qd = q.cuda()
+    out = qd if alias else torch.full_like(qd, 7.0)
+    G.cache_attention(qd, paged.dev, paged.table_t(), _i32(lens), cu_seqlens=cu, window=window, scale=scale,
+                      out=out)
+    torch.cuda.synchronize()
+    rows = f64(q).reshape(-1, Hq, paged.d)
+    few = max(lead[1] if packed else new[0], 1) * (Hq // paged.Hk) <= 32
+    ref, bound = attention_ref(rows, paged, lens, spans, window, scale, few=few)
+    if behind:
+        ref[-behind:] = rows[-behind:] if alias else 7.0
+    assert_within("o", f64(out).reshape(ref.shape), ref, bound)
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,L", [(1, 1), (4, 1), (3, 5), (8, 2), (8, 4), (16, 1), (1, 32)])
+@pytest.mark.parametrize("window", [0, 1, 70])
+def test_attention_few_rows(G, L, d, window):
+    rng = np.random.default_rng(G * 7 + L + d + window)
+    lens = [L, 64, 65, 1000, 127 + L, 449]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng)
+    say("cache_attention few rows", G, L, d, window)
+    _attention(rng, paged, [L] * len(lens), lens, 2 * G, window=window, alias=L == 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,L", [(1, 33), (4, 40), (3, 130), (5, 200)])
+@pytest.mark.parametrize("window", [0, 1, 100])
+def test_attention_many_rows(G, L, d, window):
+    rng = np.random.default_rng(G * 7 + L + d + window)
+    lens = [L, L + 64, L + 333]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng)
+    say("cache_attention many rows", G, L, d, window)
+    _attention(rng, paged, [L] * len(lens), lens, 2 * G, window=window, alias=G == 4)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("new,lens,Hq,Hk", [
+    ([1, 0, 200, 33, 64], [300, 0, 200, 40, 1000], 6, 2),
+    ([3, 0, 4, 1], [70, 9, 4, 1], 4, 4),             # packed, few rows in all
+    ([700], [700], 4, 1),
+    ([1] * 70 + [90], [200] * 70 + [90], 2, 2),
+])
+def test_attention_packed(new, lens, Hq, Hk, window):
+    rng = np.random.default_rng(len(new) + window)
+    paged = Paged(rng, lens, Hk, 64)
+    paged.fill(rng)
+    say("cache_attention packed", len(new), Hq, Hk, window)
+    _attention(rng, paged, new, lens, Hq, packed=True, window=window, behind=5)
+
+
+@pytest.mark.parametrize("L", [2, 90])
+def test_attention_padding_and_missing_blocks(L):
+    """Padding rows, an empty sequence, holes in a table, a table too short for its sequence, a
+    sequence none of whose blocks exist."""
+    rng = np.random.default_rng(L)
+    lens = [1, 0, 500, 700, 64]
+    paged = Paged(rng, lens, 2, 128, table_width=9)
+    paged.fill(rng)
+    paged.table[2, 1] = -1
+    paged.table[2, 4] = paged.P
+    paged.table[4, :] = 2 ** 31 - 1
+    say("cache_attention padding and missing blocks", L)
+    for window in (0, 40):
+        _attention(rng, paged, [L] * 5, lens, 4, window=window)
+
+
+@pytest.mark.parametrize("L", [1, 6, 100])
+def test_attention_not_finite_keys(L):
+    """A marked token makes NaN of the rows that see it, and of no others."""
+    rng = np.random.default_rng(L)
+    lens = [150, 150]
+    paged = Paged(rng, lens, 2, 64)
+    paged.fill(rng)
+    for pos in (40, 148):
+        paged.ref.k[paged.table[0, pos // B64], 1, pos % B64] = np.nan
+    paged.push()
+    say("cache_attention not finite", L)
+    for window in (0, 3):
+        out = _attention(rng, paged, [L] * 2, lens, 4, window=window)
+        assert out.isnan().any() and not out[1].isnan().any()
+
+
+@pytest.mark.parametrize("L", [1, 100])
+def test_attention_stale_bytes_behind_a_sequence(L):
+    """Keys of any code, and finite values, behind the last token of a block are never seen."""
+    rng = np.random.default_rng(L + 1)
+    lens = [130, 101]
+    paged = Paged(rng, lens, 1, 128)
+    paged.fill(rng)
+    for i, n in enumerate(lens):
+        paged.ref.k[paged.table[i, n // B64], :, n % B64:] = np.nan
+        paged.ref.v[paged.table[i, n // B64], :, n % B64:] = 448.0
+    paged.push()
+    say("cache_attention stale bytes", L)
+    _attention(rng, paged, [L] * 2, lens, 3)
+
+
+def test_attention_scales_far_apart():
+    """Blocks whose scales differ by many powers of two, tiny and large scores."""
+    rng = np.random.default_rng(21)
+    lens = [400, 257]
+    paged = Paged(rng, lens, 2, 64)
+    paged.fill(rng, spread=4.0)
+    say("cache_attention scales")
+    for L in (1, 64):
+        _attention(rng, paged, [L] * 2, lens, 4, scale=0.01)
+        _attention(rng, paged, [L] * 2, lens, 4, scale=1.0, q=draw(rng, 2, L, 4, 64, scale=0.05))
+
+
+def test_attention_long_context():
+    """Many pieces of the key axis, odd lengths."""
+    rng = np.random.default_rng(22)
+    lens = [9001, 4133]
+    paged = Paged(rng, lens, 1, 64)
+    paged.fill(rng)
+    say("cache_attention long")
+    for L, window in ((1, 0), (3, 5000), (40, 0)):
+        _attention(rng, paged, [L] * 2, lens, 4, window=window)
+
+
+def test_attention_offsets_past_32_bits():
+    """Blocks past 2^31 bytes of a cache."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(23)
+    P, Hk, d = 34000, 8, 128  # 2.2 GB of keys
+    lens = [150]
+    say("cache_attention large pool")
+    small = Paged(rng, lens, Hk, d, spare=0)
+    small.fill(rng)
+    big = [torch.zeros((P, Hk, *s), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+           for s in ((64, d), (d, 64))] + [torch.zeros((P, Hk), device="cuda") for _ in range(2)]
+    place = [P - 1 - i for i in range(small.P)]
+    for b, s in zip(big, small.dev):
+        b.view(torch.uint8)[place] = s.view(torch.uint8)
+    table = np.array([[place[t] for t in small.table[0]]], np.int32)
+    fr = torch.from_numpy(inv_freq(d)).cuda()
+    for L in (1, 70):
+        q, k, v = (draw(rng, 1, L, h, d).cuda() for h in (16, Hk, Hk))
+        outs = []
+        for cache, tb in ((big, _i32(table)), (small.dev, small.table_t())):
+            qo = G.attn_prologue(q, k, v, cache, tb, _i32(lens), fr)
+            outs.append(G.cache_attention(qo, cache, tb, _i32(lens)))
+        torch.cuda.synchronize()
+        assert torch.equal(*outs)
+        for b, s in zip(big, small.dev):
+            assert torch.equal(b.view(torch.uint8)[place], s.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- together
+
+def test_serving_run():
+    """Packed prompts, single tokens, drafts with a rollback, as a serving loop makes them; then the
+    same tokens through attention at once give the same rows within the bounds."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(31)
+    Hq, Hk, d, window = 4, 2, 64, 90
+    lens = np.array([130, 61, 5])
+    paged = Paged(rng, lens + 20, Hk, d, spare=1)
+    say("serving run")
+    fr = inv_freq(d)
+    frt = torch.from_numpy(fr).cuda()
+
+    def step(new, total, packed):
+        spans, lead, cu = _layout(new, packed)
+        q, k, v = (draw(rng, *lead, h, d).cuda() for h in (Hq, Hk, Hk))
+        qo = G.attn_prologue(q, k, v, paged.dev, paged.table_t(), _i32(total), frt, cu_seqlens=cu)
+        o = G.cache_attention(qo, paged.dev, paged.table_t(), _i32(total), cu_seqlens=cu, window=window)
+        torch.cuda.synchronize()
+        kf, vf = f64(k).reshape(-1, Hk, d), f64(v).reshape(-1, Hk, d)
+        for i, (first, n) in enumerate(spans):
+            p = int(total[i]) - n + np.arange(n)
+            R.append(paged.ref, paged.table[i], int(total[i]), R.norm_rope(kf[first:first + n], None, p, fr),
+                     vf[first:first + n])
+        kd, vd, ksd, vsd = paged.pull()
+        assert np.array_equal(ksd, paged.ref.k_scale) and np.array_equal(vsd, paged.ref.v_scale)
+        assert np.array_equal(vd, paged.ref.v)
+        assert np.count_nonzero(kd != paged.ref.k) <= 4
+        paged.ref.k[:] = kd
+        few = (lead[1] if packed else new[0]) * (Hq // Hk) <= 32
+        ref, bound = attention_ref(f64(qo).reshape(-1, Hq, d), paged, total, spans, window, few=few)
+        assert_within("o", f64(o).reshape(ref.shape), ref, bound)
+
+    step([int(n) for n in lens], lens, True)
+    for _ in range(4):
+        lens = lens + 1
+        step([1] * 3, lens, False)
+    step([4] * 3, lens + 4, False)      # drafts
+    lens = lens + np.array([4, 1, 0])   # accepted
+    step([1] * 3, lens + 1, False)
+    step([3] * 3, lens + 4, False)
+
+
+def test_serving_step_captured():
+    """Prologue and attention in one graph; tokens, lengths and table change between replays."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(32)
+    Hq, Hk, d = 8, 2, 128
+    lens = np.array([130, 610, 5, 0])
+    paged = Paged(rng, lens + 70, Hk, d)
+    paged.fill(rng)
+    say("serving step captured")
+    fr = torch.from_numpy(inv_freq(d)).cuda()
+    q, k, v = (draw(rng, 4, 1, h, d).cuda() for h in (Hq, Hk, Hk))
+    lt, tb = _i32(lens), paged.table_t()
+
+    def step(cache):
+        qo = G.attn_prologue(q, k, v, cache, tb, lt, fr)
+        return qo, G.cache_attention(qo, cache, tb, lt)
+
+    twin = G.KVCache(*(t.clone() for t in paged.dev))
+    step(G.KVCache(*(t.clone() for t in paged.dev)))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(paged.dev)
+    for i in range(4):
+        lens = lens + np.array([1, 1, 20, 1])
+        lt.copy_(_i32(lens))
+        for t in (q, k, v):
+            t.copy_(draw(rng, *t.shape))
+        ref = step(twin)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, ref)), i
+        for a, b in zip(paged.dev, twin):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_streams():
+    """Two calls in flight on streams of their own, each with its own workspace."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(33)
+    lens = [5000, 3000]
+    paged = Paged(rng, lens, 2, 64)
+    paged.fill(rng)
+    say("cache_attention two streams")
+    qs = [draw(rng, 2, n, 4, 64).cuda() for n in (1, 50)]
+    tb, lt = paged.table_t(), _i32(lens)
+    ref = [G.cache_attention(q, paged.dev, tb, lt) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = []
+    for q, st in zip(qs, streams):
+        with torch.cuda.stream(st):
+            got.append([G.cache_attention(q, paged.dev, tb, lt) for _ in range(5)])
+    torch.cuda.synchronize()
+    for r, many in zip(ref, got):
+        assert all(torch.equal(r, g) for g in many)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_sweep(seed):
+    """Seeded mixed shapes: prologue, then attention on the result."""
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([64, 128]))
+    Hk, G = int(rng.choice([1, 2, 3, 5])), int(rng.choice([1, 2, 3, 4, 7]))
+    N = int(rng.integers(1, 6))
+    packed = bool(rng.random() < 0.5)
+    if packed:
+        new = [int(x) for x in rng.integers(0, 140, N)]
+        new[0] = max(new[0], 1)
+    else:
+        new = [int(rng.choice([1, 2, 3, 8, 20, 65, 129]))] * N
+    lens = [max(0, n + int(x)) for n, x in zip(new, rng.integers(-3, 300, N))]
+    window = int(rng.choice([0, 0, 1, 33, 64, 200]))
+    paged = Paged(rng, lens, Hk, d)
+    paged.fill(rng)
+    say("attention layer sweep", seed, d, Hk, G, new, lens, window)
+    _prologue(rng, paged, new, lens, Hk * G, packed, int(rng.choice([0, 16, d])), il=bool(rng.random() < 0.5))
+    _attention(rng, paged, new, lens, Hk * G, packed=packed, window=window)
