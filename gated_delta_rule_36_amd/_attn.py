@@ -8,7 +8,6 @@ library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 import math
 from typing import NamedTuple
@@ -49,19 +48,23 @@ def value_columns(device=None):
     return (t // 4 % 4) * 16 + (t // 16) * 4 + t % 4
 
 
-# Current device unchanged where it is the tensors' own (the usual call pays nothing).
-def _on(device):
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call(name, device, *args):
+    """The entry point `name` with torch's current stream of `device` behind args, that device
+    being current meanwhile. (The raw getters: torch.cuda's objects for the same cost 2 us of a
+    small call's 10.)"""
+    fn = getattr(lib(), name)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise Gdn2Error(name, st)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need_gpu(t):
@@ -69,24 +72,27 @@ def _need_gpu(t):
         raise ValueError("tensors must be on a HIP device")
 
 
-def _code(dt):
-    if dt == torch.bfloat16:
-        return GDN2_BF16
-    if dt == torch.float32:
-        return GDN2_F32
-    raise TypeError(f"unsupported dtype {dt}; use bfloat16 or float32")
+_CODES = {torch.bfloat16: GDN2_BF16, torch.float32: GDN2_F32}
 
 
-def _rows(name, t, lead, dtype, device):
+def _bad(name, t, shape, dtype, device):
+    want = f"a {dtype} tensor of shape {tuple(shape)} on {device}"
+    err = TypeError if t.dtype != dtype else ValueError
+    raise err(f"{name}: expected {want}, got {t.dtype} {tuple(t.shape)} on {t.device}, "
+              f"strides {t.stride()}")
+
+
+def _dense(name, t, shape, dtype, device):
+    if not t.is_contiguous() or t.shape != shape or t.dtype != dtype or t.device != device:
+        _bad(name + " (contiguous)", t, shape, dtype, device)
+
+
+def _rows(name, t, shape, dtype, device):
     """Checks [B, T, H, d] rows whose tokens lie at one stride with dense heads; returns that
     stride in elements."""
-    if t.dim() != 4 or t.shape[:2] != lead:
-        raise ValueError(f"{name}: expected shape {tuple(lead)} + (H, d), got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    B, T, H, d = t.shape
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _bad(name, t, shape, dtype, device)
+    B, T, H, d = shape
     if t.is_contiguous():
         return H * d
     sb, st, sh, sd = t.stride()
@@ -101,47 +107,44 @@ def _rows(name, t, lead, dtype, device):
     return st
 
 
-def _vector(name, t, shape, dtype, device):
-    if t is None:
-        return
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _dense(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _empty(t, stride):
+    """A contiguous tensor like t, whose tokens lie at `stride`."""
+    if stride == t.shape[2] * t.shape[3]:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _rotation(inv_freq, d, dev):
     """rot, after a check of inv_freq [rot / 2] (None: no rotation)."""
     if inv_freq is None:
         return 0
-    rot = 2 * inv_freq.numel()
-    _vector("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
-    if rot > d or rot % 8:
-        raise ValueError(f"inv_freq: {rot} rotated channels; a multiple of 8 up to {d} is needed")
-    return rot
+    half = inv_freq.numel()
+    _dense("inv_freq", inv_freq, (half,), torch.float32, dev)
+    if 2 * half > d or half % 4:
+        raise ValueError(f"inv_freq: {2 * half} rotated channels; a multiple of 8 up to {d} is "
+                         f"needed")
+    return 2 * half
 
 
 def _norm_rope_args(q, k, inv_freq, positions, q_weight, k_weight):
     _need_gpu(q)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, T, H, d]")
-    B, T, Hq, d = q.shape
+    B, T, Hq, d = shape = q.shape
+    Hk = k.shape[2]
     dev, dt = q.device, q.dtype
-    code = _code(dt)
-    qs = _rows("q", q, (B, T), dt, dev)
-    ks = _rows("k", k, (B, T), dt, dev)
-    if k.shape[3] != d:
-        raise ValueError(f"k: head width {k.shape[3]}, q has {d}")
-    _vector("positions", positions, (B, T), torch.int32, dev)
-    _vector("q_weight", q_weight, (d,), torch.float32, dev)
-    _vector("k_weight", k_weight, (d,), torch.float32, dev)
-    rot = _rotation(inv_freq, d, dev)
-    return B, T, Hq, k.shape[2], d, qs, ks, rot, code, dev, dt
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}; use bfloat16 or float32")
+    qs = _rows("q", q, shape, dt, dev)
+    ks = _rows("k", k, (B, T, Hk, d), dt, dev)
+    if positions is not None:
+        _dense("positions", positions, (B, T), torch.int32, dev)
+    if q_weight is not None:
+        _dense("q_weight", q_weight, (d,), torch.float32, dev)
+    if k_weight is not None:
+        _dense("k_weight", k_weight, (d,), torch.float32, dev)
+    return B, T, Hq, Hk, d, qs, ks, _rotation(inv_freq, d, dev), code, dev, dt
 
 
 def _flags(interleaved, norm):
@@ -162,19 +165,20 @@ def qk_norm_rope_fwd(q, k, inv_freq, positions=None, q_weight=None, k_weight=Non
     B, T, Hq, Hk, d, qs, ks, rot, code, dev, dt = _norm_rope_args(q, k, inv_freq, positions,
                                                                   q_weight, k_weight)
     if out is None:
-        qo = torch.empty((B, T, Hq, d), dtype=dt, device=dev)
-        ko = torch.empty((B, T, Hk, d), dtype=dt, device=dev)
+        qo, ko = _empty(q, qs), _empty(k, ks)
     else:
         qo, ko = out
         _dense("out[0]", qo, (B, T, Hq, d), dt, dev)
         _dense("out[1]", ko, (B, T, Hk, d), dt, dev)
-    with _on(dev):
-        st = lib().gdn2_qk_norm_rope(_p(q), _p(k), _p(q_weight), _p(k_weight), _p(positions),
-                                     _p(inv_freq), _p(qo), _p(ko), B, T, Hq, Hk, d, qs, ks, rot,
-                                     eps, _flags(interleaved, norm), code, _stream(dev))
-    if st != 0:
-        raise Gdn2Error("gdn2_qk_norm_rope", st)
+    _call("gdn2_qk_norm_rope", dev, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
+          _p(positions), _p(inv_freq), qo.data_ptr(), ko.data_ptr(), B, T, Hq, Hk, d, qs, ks, rot,
+          eps, _flags(interleaved, norm), code)
     return qo, ko
+
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_workspace(B, T, Hq, Hk, d):
+    return int(lib().gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d))
 
 
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq, positions=None, q_weight=None, k_weight=None,
@@ -185,23 +189,18 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq, positions=None, q_weight=No
                                                                   q_weight, k_weight)
     _dense("dq_out", dq_out, (B, T, Hq, d), dt, dev)
     _dense("dk_out", dk_out, (B, T, Hk, d), dt, dev)
-    dq = torch.empty((B, T, Hq, d), dtype=dt, device=dev)
-    dk = torch.empty((B, T, Hk, d), dtype=dt, device=dev)
+    dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
     make = torch.empty if B * T else torch.zeros
     dwq = make(d, dtype=torch.float32, device=dev) if q_weight is not None else None
     dwk = make(d, dtype=torch.float32, device=dev) if k_weight is not None else None
-    L = lib()
     ws, need = None, 0
     if dwq is not None or dwk is not None:
-        need = int(L.gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d))
+        need = _bwd_workspace(B, T, Hq, Hk, d)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = L.gdn2_qk_norm_rope_bwd(_p(q), _p(k), _p(dq_out), _p(dk_out), _p(q_weight),
-                                     _p(k_weight), _p(positions), _p(inv_freq), _p(dq), _p(dk),
-                                     _p(dwq), _p(dwk), B, T, Hq, Hk, d, qs, ks, rot, eps,
-                                     _flags(interleaved, norm), code, _p(ws), need, _stream(dev))
-    if st != 0:
-        raise Gdn2Error("gdn2_qk_norm_rope_bwd", st)
+    _call("gdn2_qk_norm_rope_bwd", dev, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(),
+          dk_out.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
+          dq.data_ptr(), dk.data_ptr(), _p(dwq), _p(dwk), B, T, Hq, Hk, d, qs, ks, rot, eps,
+          _flags(interleaved, norm), code, _p(ws), need)
     return dq, dk, dwq, dwk
 
 
@@ -239,14 +238,13 @@ def _cache_args(q, cache, block_table, seq_lens, cu_seqlens):
     if q.dtype != torch.bfloat16:
         raise TypeError(f"the cached attention layer is built for bfloat16, got {q.dtype}")
     kc, vc, ks, vs = cache
-    if kc.dim() != 4 or vc.dim() != 4:
+    if kc.dim() != 4:
         raise ValueError("cache: k must be [P, Hk, 64, d] and v [P, Hk, d, 64]")
     P, Hk = kc.shape[:2]
-    for name, t, shape, dt in (("cache.k", kc, (P, Hk, CACHE_BLOCK, d), torch.float8_e4m3fn),
-                               ("cache.v", vc, (P, Hk, d, CACHE_BLOCK), torch.float8_e4m3fn),
-                               ("cache.k_scale", ks, (P, Hk), torch.float32),
-                               ("cache.v_scale", vs, (P, Hk), torch.float32)):
-        _dense(name, t, shape, dt, dev)
+    _dense("cache.k", kc, (P, Hk, CACHE_BLOCK, d), torch.float8_e4m3fn, dev)
+    _dense("cache.v", vc, (P, Hk, d, CACHE_BLOCK), torch.float8_e4m3fn, dev)
+    _dense("cache.k_scale", ks, (P, Hk), torch.float32, dev)
+    _dense("cache.v_scale", vs, (P, Hk), torch.float32, dev)
     if Hq % Hk:
         raise ValueError(f"{Hq} query heads cannot share {Hk} kv heads evenly")
     if cu_seqlens is not None:
@@ -281,27 +279,24 @@ def attn_prologue(q, k, v, cache, block_table, seq_lens, inv_freq, cu_seqlens=No
     that is written. out: optional contiguous result, which may be q.
     Returns q_out, [.., Hq, d]."""
     B, T, Hq, Hk, d, N, P, MB, dev = _cache_args(q, cache, block_table, seq_lens, cu_seqlens)
-    qs = _rows("q", q, (B, T), torch.bfloat16, dev)
-    ks = _rows("k", k, (B, T), torch.bfloat16, dev)
-    vs = _rows("v", v, (B, T), torch.bfloat16, dev)
-    if k.shape[2:] != (Hk, d) or v.shape[2:] != (Hk, d):
-        raise ValueError(f"k and v must have {Hk} heads of {d} channels, got {tuple(k.shape)} and "
-                         f"{tuple(v.shape)}")
-    _vector("q_weight", q_weight, (d,), torch.float32, dev)
-    _vector("k_weight", k_weight, (d,), torch.float32, dev)
+    qs = _rows("q", q, (B, T, Hq, d), torch.bfloat16, dev)
+    ks = _rows("k", k, (B, T, Hk, d), torch.bfloat16, dev)
+    vs = _rows("v", v, (B, T, Hk, d), torch.bfloat16, dev)
+    if q_weight is not None:
+        _dense("q_weight", q_weight, (d,), torch.float32, dev)
+    if k_weight is not None:
+        _dense("k_weight", k_weight, (d,), torch.float32, dev)
     rot = _rotation(inv_freq, d, dev)
     if out is None:
-        out = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=dev)
+        out = _empty(q, qs)
     else:
         _dense("out", out, (B, T, Hq, d), torch.bfloat16, dev)
-    with _on(dev):
-        st = lib().gdn2_attn_prologue(
-            _p(q), _p(k), _p(v), _p(q_weight), _p(k_weight), _p(inv_freq), _p(out), _p(cache[0]),
-            _p(cache[1]), _p(cache[2]), _p(cache[3]), _p(block_table), _p(seq_lens),
-            _p(cu_seqlens), B, T, Hq, Hk, d, N, P, MB, qs, ks, vs, rot, eps,
-            _flags(interleaved, norm), GDN2_BF16, _stream(dev))
-    if st != 0:
-        raise Gdn2Error("gdn2_attn_prologue", st)
+    kc, vc, kcs, vcs = cache
+    _call("gdn2_attn_prologue", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(q_weight),
+          _p(k_weight), _p(inv_freq), out.data_ptr(), kc.data_ptr(), vc.data_ptr(),
+          kcs.data_ptr(), vcs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+          _p(cu_seqlens), B, T, Hq, Hk, d, N, P, MB, qs, ks, vs, rot, eps,
+          _flags(interleaved, norm), GDN2_BF16)
     return out
 
 
@@ -342,13 +337,11 @@ def cache_attention(q, cache, block_table, seq_lens, cu_seqlens=None, window=0, 
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    with _on(dev):
-        st = lib().gdn2_cache_attention(
-            _p(q), _p(cache[0]), _p(cache[1]), _p(cache[2]), _p(cache[3]), _p(block_table),
-            _p(seq_lens), _p(cu_seqlens), _p(out), B, T, Hq, Hk, d, N, P, MB, window, scale,
-            GDN2_BF16, _p(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
-    if st != 0:
-        raise Gdn2Error("gdn2_cache_attention", st)
+    kc, vc, ks, vs = cache
+    _call("gdn2_cache_attention", dev, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+          vs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _p(cu_seqlens),
+          out.data_ptr(), B, T, Hq, Hk, d, N, P, MB, window, scale, GDN2_BF16, _p(workspace),
+          0 if workspace is None else workspace.numel())
     return out
 
 

@@ -28,6 +28,7 @@ namespace gdn2 {
 namespace {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t lo, uint32_t hi, float 
 
 // Block b of sequence n: its slot, or -1 where the table names none.
 __device__ __forceinline__ int block_slot(const CacheView& C, const int* table, int b) {
-  const int s = table[b];
+  const int s = scalar_load(table, b);
   return (unsigned)s < (unsigned)C.P ? s : -1;
 }
 
@@ -62,10 +63,10 @@ struct Pieces {
 
 // ---------------------------------------------------------------- few rows
 
-// grid N * Hk * splits; 4 waves, wave w takes blocks w, w + 4, ... of the piece. RT tiles of 16
+// grid N * Hk * splits; NW waves, wave w takes blocks w, w + NW, ... of the piece. RT tiles of 16
 // query rows; row r is query token r / G, head h G + r % G. LDS only for the merge of the waves.
-template <int D, int RT>
-__global__ void __launch_bounds__(256)
+template <int D, int RT, int NW>
+__global__ void __launch_bounds__(NW * 64, 2)
 gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
   constexpr int KH = D / 64;   // 64-channel halves of a key row
   constexpr int DT = D / 16;   // value tiles
@@ -76,6 +77,10 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
   const int nh = blockIdx.x / W.splits;
   const int h = nh % A.Hk, n = nh / A.Hk;
   const int G = A.Hq / A.Hk;
+  const int* table = C.block_table + (long)n * C.max_blocks;
+  // without a window the first block is known before the length is: one wait for both
+  const int e = piece * split_blocks + wave;
+  const int early = A.window > 0 ? -1 : block_slot(C, table, e < C.max_blocks ? e : 0);
   const SeqSpan s = seq_span(C, n);
   const int rows = s.count * G < RT * 16 ? s.count * G : RT * 16;
   if (rows == 0) return;
@@ -91,7 +96,7 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
     return ((long)s.first + r / G) * A.Hq + h * G + r % G;
   };
   if (b0 >= b1) {  // nothing here: an empty piece (the only one: zeros)
-    for (int r = threadIdx.x / 16; r < rows; r += 16) {
+    for (int r = threadIdx.x / 16; r < rows; r += NW * 4) {
       if (W.splits == 1) {
         for (int d = (threadIdx.x % 16) * 8; d < D; d += 128)
           *reinterpret_cast<uint4*>((bf16*)A.o + row_index(r) * D + d) = make_uint4(0, 0, 0, 0);
@@ -120,7 +125,6 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
         qf[t][k][u] = *reinterpret_cast<const bf16x8*>(qr + k * 64 + c * 16 + u * 8);
   }
 
-  const int* table = C.block_table + (long)n * C.max_blocks;
   const float scale = A.scale * kLog2e;
   f4 o[RT][DT];
   float m[RT], l[RT];
@@ -132,38 +136,43 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
     for (int i = 0; i < DT; ++i) o[t][i] = f4{0.f, 0.f, 0.f, 0.f};
   }
 
-  uint4 kr[4][KH], vr[DT];
-  float ks = 1.f, vs = 1.f;
-  auto load_k = [&](int slot) {
+  struct Block {  // a block's codes as a lane holds them
+    uint4 k[4][KH], v[DT];
+    float ks, vs;
+  };
+  auto load_k = [&](Block& r, int slot) {
     const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
     const uint8_t* p = C.k + head * (kCacheBlock * D) + col * D + c * 16;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int k = 0; k < KH; ++k)
-        kr[t][k] = *reinterpret_cast<const uint4*>(p + t * 16 * D + k * 64);
-    ks = C.k_scale[head];
+        r.k[t][k] = *reinterpret_cast<const uint4*>(p + t * 16 * D + k * 64);
+    r.ks = scalar_load(C.k_scale, head);
   };
-  auto load_v = [&](int slot) {
+  auto load_v = [&](Block& r, int slot) {
     const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
     const uint8_t* p = C.v + head * (kCacheBlock * D) + col * kCacheBlock + c * 16;
 #pragma unroll
     for (int i = 0; i < DT; ++i)
-      vr[i] = *reinterpret_cast<const uint4*>(p + i * 16 * kCacheBlock);
-    vs = C.v_scale[head];
+      r.v[i] = *reinterpret_cast<const uint4*>(p + i * 16 * kCacheBlock);
+    r.vs = scalar_load(C.v_scale, head);
   };
 
+  // One block's registers, refilled as they are consumed: a second set (the next block's loads
+  // before this one's arithmetic) measured 2 to 5% slower.
   int b = b0 + wave;
   int slot = -1, next = -1;
+  Block cur;
   if (b < b1) {
-    slot = block_slot(C, table, b);
-    load_k(slot);
-    load_v(slot);
-    if (b + 4 < b1) next = block_slot(C, table, b + 4);
+    slot = A.window > 0 ? block_slot(C, table, b) : early;
+    load_k(cur, slot);
+    load_v(cur, slot);
+    if (b + NW < b1) next = block_slot(C, table, b + NW);
   }
-  for (; b < b1; b += 4) {
+  for (; b < b1; b += NW) {
     int after = -1;
-    if (b + 8 < b1) after = block_slot(C, table, b + 8);
+    if (b + 2 * NW < b1) after = block_slot(C, table, b + 2 * NW);
     f4 sc[RT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -171,8 +180,8 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
       for (int q = 0; q < RT; ++q) sc[q][t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KH; ++k) {
-        const bf16x8 k0 = codes_to_bf16(kr[t][k].x, kr[t][k].y, ks);
-        const bf16x8 k1 = codes_to_bf16(kr[t][k].z, kr[t][k].w, ks);
+        const bf16x8 k0 = codes_to_bf16(cur.k[t][k].x, cur.k[t][k].y, cur.ks);
+        const bf16x8 k1 = codes_to_bf16(cur.k[t][k].z, cur.k[t][k].w, cur.ks);
 #pragma unroll
         for (int q = 0; q < RT; ++q) {
           sc[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[q][k][0], sc[q][t], 0, 0, 0);
@@ -180,7 +189,7 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
         }
       }
     }
-    if (b + 4 < b1) load_k(next);
+    if (b + NW < b1) load_k(cur, next);
 
     const int key0 = b * kCacheBlock;
     if (slot < 0 || key0 + kCacheBlock - 1 > p0 ||
@@ -232,8 +241,8 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
     }
 #pragma unroll
     for (int i = 0; i < DT; ++i) {
-      const bf16x8 v0 = codes_to_bf16(vr[i].x, vr[i].y, vs);
-      const bf16x8 v1 = codes_to_bf16(vr[i].z, vr[i].w, vs);
+      const bf16x8 v0 = codes_to_bf16(cur.v[i].x, cur.v[i].y, cur.vs);
+      const bf16x8 v1 = codes_to_bf16(cur.v[i].z, cur.v[i].w, cur.vs);
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         o[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[q][0], o[q][i], 0, 0, 0);
@@ -242,14 +251,14 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
         o[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[q][1], o[q][i], 0, 0, 0);
       }
     }
-    if (b + 4 < b1) load_v(next);
+    if (b + NW < b1) load_v(cur, next);
     slot = next;
     next = after;
   }
 
-  // Merge of the four waves, a tile of rows at a time.
-  __shared__ float sm[4][RT * 16], sl[4][RT * 16];
-  __shared__ __align__(16) float so[4][16][D + 4];
+  // Merge of the waves, a tile of rows at a time.
+  __shared__ float sm[NW][RT * 16], sl[NW][RT * 16];
+  __shared__ __align__(16) float so[NW][16][D + 4];
 #pragma unroll
   for (int q = 0; q < RT; ++q) {
     l[q] += __shfl_xor(l[q], 16, 64);
@@ -259,12 +268,14 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
       sl[wave][q * 16 + col] = l[q];
     }
   }
-  const int tr = threadIdx.x >> 4, ts = threadIdx.x & 15;
+  constexpr int TPR = NW * 4, E = D / TPR;  // threads a row, channels a thread
+  const int tr = threadIdx.x / TPR, ts = threadIdx.x % TPR;
 #pragma unroll
   for (int q = 0; q < RT; ++q) {
     __syncthreads();
-    const int rc = q * 16 + col;
-    const float top = fmaxf(fmaxf(sm[0][rc], sm[1][rc]), fmaxf(sm[2][rc], sm[3][rc]));
+    float top = kNegInf;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, sm[w][q * 16 + col]);
     const float f = m[q] == kNegInf ? 0.f : exp2_f(m[q] - top);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
@@ -272,31 +283,25 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
     __syncthreads();
     const int r = q * 16 + tr;
     if (r >= rows) continue;
-    const float mt = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-    float lt = 0.f;
+    float mt = kNegInf, lt = 0.f, x[E] = {};
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = 0; w < NW; ++w) mt = fmaxf(mt, sm[w][r]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
       lt += sl[w][r] * (sm[w][r] == kNegInf ? 0.f : exp2_f(sm[w][r] - mt));
-    const long out = row_index(r);
-    constexpr int E = D / 16;  // channels a thread
-    float x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      x[i] = (so[0][tr][ts * E + i] + so[1][tr][ts * E + i]) +
-             (so[2][tr][ts * E + i] + so[3][tr][ts * E + i]);
+      for (int i = 0; i < E; ++i) x[i] += so[w][tr][ts * E + i];
+    }
+    const long out = row_index(r);
     if (W.splits == 1) {
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
       bf16* dst = (bf16*)A.o + out * D + ts * E;
 #pragma unroll
-      for (int i = 0; i < E; i += 4)
-        *reinterpret_cast<bf16x4*>(dst + i) =
-            bf16x4{static_cast<bf16>(x[i] * inv), static_cast<bf16>(x[i + 1] * inv),
-                   static_cast<bf16>(x[i + 2] * inv), static_cast<bf16>(x[i + 3] * inv)};
+      for (int i = 0; i < E; ++i) dst[i] = static_cast<bf16>(x[i] * inv);
     } else {
       float* dst = W.o + ((long)piece * W.rows + out) * D + ts * E;
 #pragma unroll
-      for (int i = 0; i < E; i += 4)
-        *reinterpret_cast<f4*>(dst + i) = f4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+      for (int i = 0; i < E; ++i) dst[i] = x[i];
       if (ts == 0) {
         float* ml = W.ml + ((long)piece * W.rows + out) * 2;
         ml[0] = mt;
@@ -308,18 +313,21 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
 
 // ---------------------------------------------------------------- many rows
 
-constexpr int kTileRows = 128;
-
-// grid splits * units * Hk; a unit is one 128-row tile of a sequence, the last tiles (with the
+// grid splits * units * Hk; a unit is one tile of 32 NW rows of a sequence, the last tiles (with the
 // most keys) first. Wave w owns rows 32 w ..; lane: query row (lane % 32), half hf = lane / 32.
-template <int D>
-__global__ void __launch_bounds__(256, 2)
-gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int tiles_per_seq, Pieces W) {
+//
+// The loop is pipelined over two blocks: the softmax of block b (VALU, exp2 above all) runs beside
+// the products K(b + 1) Q^T, and the maximum of b + 1 and the staging of K(b + 2) and V(b + 1)
+// beside V(b)^T P(b)^T, so that the matrix cores have work throughout.
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 64, 2)
+gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces W) {
+  constexpr int ROWS = 32 * NW;   // rows of a workgroup
   constexpr int QS = D / 16;       // K steps of the score product
   constexpr int DT = D / 32;       // value tiles
   constexpr int KLD = D + 8;       // LDS rows padded by 16 bytes: reads of 8 rows a phase hit
   constexpr int VLD = kCacheBlock + 8;  // every bank once
-  constexpr int NC = kCacheBlock * D / 16 / 256;  // 16-byte chunks a thread stages
+  constexpr int NT = NW * 64, NC = kCacheBlock * D / 16 / NT;  // 16-byte chunks a thread stages
   __shared__ __align__(16) bf16 lk[2][kCacheBlock * KLD];
   __shared__ __align__(16) bf16 lv[2][D * VLD];
   const CacheView& C = A.c;
@@ -335,37 +343,33 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int tiles_per_seq, Piece
     tile = unit / C.N;
   } else {
     n = wave_search(C.N, unit, [&](int i) {
-      return (long)clamped_offset(C.cu_seqlens, i, C.T) * G / kTileRows + i;
+      return (long)clamped_offset(C.cu_seqlens, i, C.T) * G / ROWS + i;
     });
-    tile = unit - (int)((long)clamped_offset(C.cu_seqlens, n, C.T) * G / kTileRows) - n;
+    tile = unit - (int)((long)clamped_offset(C.cu_seqlens, n, C.T) * G / ROWS) - n;
   }
   const SeqSpan s = seq_span(C, n);
   const long rows = (long)s.count * G;
-  const long row0 = (long)tile * kTileRows;
+  const long row0 = (long)tile * ROWS;
   if (tile < 0 || row0 >= rows) return;
-  const long row_end = row0 + kTileRows < rows ? row0 + kTileRows : rows;
+  const long row_end = row0 + ROWS < rows ? row0 + ROWS : rows;
   const int p0 = s.len - s.count;  // position of the first query of the sequence
   const int pmin = p0 + (int)(row0 / G), pmax = p0 + (int)((row_end - 1) / G);
   const long span = (long)C.max_blocks * kCacheBlock;
   const int hi = pmax + 1 < span ? pmax + 1 : (int)span;
   int b0 = (below_window(pmin, A.window) + 1) / kCacheBlock;
   int b1 = hi > 0 ? (hi + kCacheBlock - 1) / kCacheBlock : 0;
-  if (W.splits > 1 && b1 > b0) {
-    const int per = (b1 - b0 + W.splits - 1) / W.splits;
-    b0 += piece * per;
-    b1 = b1 < b0 + per ? b1 : b0 + per;
-  }
+  b0 += piece * split_blocks;
+  if (b1 > b0 + split_blocks) b1 = b0 + split_blocks;
 
-  const long r = row0 + wave * 32 + col;
+  const long wr0 = row0 + wave * 32;  // positions that this wave's rows span (uniform)
+  const long wr1 = wr0 + 32 < rows ? wr0 + 32 : rows;
+  const int wmin = wr0 < rows ? p0 + (int)(wr0 / G) : -1;
+  const int wmax = wr0 < rows ? p0 + (int)((wr1 - 1) / G) : -1;
+  const long r = wr0 + col;
   const bool live = r < rows;
   const int pos = live ? p0 + (int)(r / G) : -1;
-  const long out = ((long)s.first + (live ? r / G : 0)) * A.Hq + h * G + (live ? r % G : 0);
-  // positions that this wave's rows span (uniform)
-  const long wr0 = row0 + wave * 32;
-  const int wmin = wr0 < rows ? p0 + (int)(wr0 / G) : -1;
-  const int wmax = wr0 < rows ? p0 + (int)(((wr0 + 31 < rows ? wr0 + 31 : rows - 1)) / G) : -1;
   const int low = below_window(pos, A.window);
-
+  const long out = ((long)s.first + (live ? r / G : 0)) * A.Hq + h * G + (live ? r % G : 0);
   bf16x8 qf[QS];
   {
     const bf16* qr = (const bf16*)A.q + out * D + hf * 8;
@@ -374,124 +378,198 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int tiles_per_seq, Piece
   }
   const float scale = A.scale * kLog2e;
   f16v o[DT];
+  float m = kNegInf, l = 0.f;
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-  float m = kNegInf, l = 0.f;
 
   const int* table = C.block_table + (long)n * C.max_blocks;
   uint4 kreg[NC], vreg[NC];
   float ks = 1.f, vs = 1.f;
-  auto fetch = [&](int slot) {
+  auto fetch_k = [&](int slot) {
     const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
-    const uint4* pk = reinterpret_cast<const uint4*>(C.k + head * (kCacheBlock * D));
-    const uint4* pv = reinterpret_cast<const uint4*>(C.v + head * (kCacheBlock * D));
+    const uint4* p = reinterpret_cast<const uint4*>(C.k + head * (kCacheBlock * D));
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      kreg[j] = pk[tid + j * 256];
-      vreg[j] = pv[tid + j * 256];
-    }
-    ks = C.k_scale[head];
-    vs = C.v_scale[head];
+    for (int j = 0; j < NC; ++j) kreg[j] = p[tid + j * NT];
+    ks = scalar_load(C.k_scale, head);
   };
-  // Chunks to LDS as bf16. Value chunk cc holds the 4-token groups (t, cc), keys 16 t + 4 cc ..:
-  // they go where the lane of half cc & 1 reads step t of the second product.
-  auto put = [&](int buf) {
+  auto fetch_v = [&](int slot) {
+    const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
+    const uint4* p = reinterpret_cast<const uint4*>(C.v + head * (kCacheBlock * D));
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int i = tid + j * 256;
-      bf16* dk = &lk[buf][(i / (D / 16)) * KLD + (i % (D / 16)) * 16];
-      *reinterpret_cast<bf16x8*>(dk) = codes_to_bf16(kreg[j].x, kreg[j].y, ks);
-      *reinterpret_cast<bf16x8*>(dk + 8) = codes_to_bf16(kreg[j].z, kreg[j].w, ks);
-      const int cc = i & 3;
-      bf16* dv = &lv[buf][(i >> 2) * VLD + (cc & 1) * 8 + (cc >> 1) * 4];
-      const bf16x8 a = codes_to_bf16(vreg[j].x, vreg[j].y, vs);
-      const bf16x8 b = codes_to_bf16(vreg[j].z, vreg[j].w, vs);
-      *reinterpret_cast<bf16x4*>(dv) = __builtin_shufflevector(a, a, 0, 1, 2, 3);
-      *reinterpret_cast<bf16x4*>(dv + 16) = __builtin_shufflevector(a, a, 4, 5, 6, 7);
-      *reinterpret_cast<bf16x4*>(dv + 32) = __builtin_shufflevector(b, b, 0, 1, 2, 3);
-      *reinterpret_cast<bf16x4*>(dv + 48) = __builtin_shufflevector(b, b, 4, 5, 6, 7);
-    }
+    for (int j = 0; j < NC; ++j) vreg[j] = p[tid + j * NT];
+    vs = scalar_load(C.v_scale, head);
   };
+  auto put_codes = [&](int buf, int j, const uint4& x, float scale_k) {
+    const int i = tid + j * NT;
+    bf16* dk = &lk[buf][(i / (D / 16)) * KLD + (i % (D / 16)) * 16];
+    *reinterpret_cast<bf16x8*>(dk) = codes_to_bf16(x.x, x.y, scale_k);
+    *reinterpret_cast<bf16x8*>(dk + 8) = codes_to_bf16(x.z, x.w, scale_k);
+  };
+  auto put_k = [&](int buf, int j) { put_codes(buf, j, kreg[j], ks); };
+  // Value chunk cc holds the 4-token groups (t, cc), keys 16 t + 4 cc ..: they go where the lane
+  // of half cc & 1 reads step t of the second product.
+  auto put_v = [&](int buf, int j) {
+    const int i = tid + j * NT;
+    const int cc = i & 3;
+    bf16* dv = &lv[buf][(i >> 2) * VLD + (cc & 1) * 8 + (cc >> 1) * 4];
+    const bf16x8 a = codes_to_bf16(vreg[j].x, vreg[j].y, vs);
+    const bf16x8 b = codes_to_bf16(vreg[j].z, vreg[j].w, vs);
+    *reinterpret_cast<bf16x4*>(dv) = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+    *reinterpret_cast<bf16x4*>(dv + 16) = __builtin_shufflevector(a, a, 4, 5, 6, 7);
+    *reinterpret_cast<bf16x4*>(dv + 32) = __builtin_shufflevector(b, b, 0, 1, 2, 3);
+    *reinterpret_cast<bf16x4*>(dv + 48) = __builtin_shufflevector(b, b, 4, 5, 6, 7);
+  };
+  // Fragment of K step k (u = k / 2: channels 16 u .., t = k % 2: keys 32 t ..) and of V step v
+  // (u = v / DT: keys 16 u .., tile v % DT: channels 32 ..).
+  auto k_frag = [&](int buf, int k) {
+    return *reinterpret_cast<const bf16x8*>(
+        &lk[buf][((k & 1) * 32 + col) * KLD + (k >> 1) * 16 + hf * 8]);
+  };
+  auto v_frag = [&](int buf, int v) {
+    return *reinterpret_cast<const bf16x8*>(
+        &lv[buf][((v % DT) * 32 + col) * VLD + (v / DT) * 16 + hf * 8]);
+  };
+  constexpr int STEPS = 2 * QS;  // of either product
+  static_assert(STEPS == 4 * DT, "as many K fragments as V fragments");
 
-  int slot = -1, next = -1;
   if (b0 < b1) {
-    slot = block_slot(C, table, b0);
-    fetch(slot);
-    if (b0 + 1 < b1) next = block_slot(C, table, b0 + 1);
-    put(0);
-  }
-  __syncthreads();
-  for (int b = b0; b < b1; ++b) {
-    const int buf = (b - b0) & 1;
-    const bool more = b + 1 < b1;
-    int after = -1;
-    if (more) fetch(next);
-    if (b + 2 < b1) after = block_slot(C, table, b + 2);
-    const int key0 = b * kCacheBlock;
-    // rows of this wave that see something of the block
-    if (slot >= 0 && key0 <= wmax && key0 + kCacheBlock - 1 > below_window(wmin, A.window)) {
-      f16v sc[2];
+    f16v sa[2], sb[2];  // scores of one block and of the next, in turn
+    // (indices past the last block repeat it: the loads do not wait for a branch)
+    const int e = b1 - 1;
+    int s0 = block_slot(C, table, b0), s1 = block_slot(C, table, b0 + 1 < b1 ? b0 + 1 : e),
+        s2 = block_slot(C, table, b0 + 2 < b1 ? b0 + 2 : e);
+    // K(b0), K(b0 + 1) and V(b0) in one wait
+    fetch_k(s0);
+    const float ks0 = ks;
+    uint4 k0[NC];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+    for (int j = 0; j < NC; ++j) k0[j] = kreg[j];
+    fetch_k(s1);
+    fetch_v(s0);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sc[t][j] = 0.f;
+    for (int j = 0; j < NC; ++j) put_codes(0, j, k0[j], ks0);
 #pragma unroll
-        for (int u = 0; u < QS; ++u) {
-          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(
-              &lk[buf][(t * 32 + col) * KLD + u * 16 + hf * 8]);
-          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u], sc[t], 0, 0, 0);
-        }
-      }
-      if (key0 + kCacheBlock - 1 > wmin || key0 <= below_window(wmax, A.window)) {
+    for (int j = 0; j < NC; ++j) {
+      put_k(1, j);
+      put_v(0, j);
+    }
+    fetch_k(s2);
+    fetch_v(s1);
+    __syncthreads();
+    const f16v zero = {};
+    constexpr int AHEAD = 2;  // fragments are read two steps before their product
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+      sa[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(0, k), qf[k >> 1],
+                                                          k < 2 ? zero : sa[k & 1], 0, 0, 0);
+    // Scores of block b that the masks leave; only blocks on the edge of some row's range need it.
+    auto mask = [&](f16v* x, int b, int slot) {
+      const int key0 = b * kCacheBlock;
+      if (slot < 0 || key0 + kCacheBlock - 1 > wmin || key0 <= below_window(wmax, A.window)) {
+        const int last = slot < 0 ? -1 : pos;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int key = key0 + t * 32 + (j >> 2) * 8 + hf * 4 + (j & 3);
-            if (key > pos || key <= low) sc[t][j] = kNegInf;
+            x[t][j] = (key > last) | (key <= low) ? kNegInf : x[t][j];
           }
       }
-      float top = kNegInf;
+    };
+    auto joined = [&](float x) {  // maximum over the two lanes of a row
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x),
+                                                       false, false);
+      return fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+    };
+    mask(sa, b0, s0);
+    float top = kNegInf;  // maximum of the block whose softmax is next
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[t][j]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float mn = fmaxf(m, top * scale);
-      const float base = mn == kNegInf ? 0.f : mn;
-      const float alpha = exp2_f(m - base);
-      m = mn;
-      float sum = 0.f;
-      bf16x8 pf[4];
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, sa[t][j]);
+    top = joined(top);
+    __syncthreads();
+
+    // Block b: sc its scores, sn the place of the next one's. One product a step; the fences
+    // keep the VALU work spread between them (left alone, the compiler gathers it behind).
+    auto iterate = [&](f16v* sc, f16v* sn, int b) {
+      const int buf = (b - b0) & 1;
+      bf16x8 kf[3], vf[3];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          // one rounding of the weight to bf16 (at most 2^-8 of it), the matrix cores' input type
-          const float p = exp2_f(fmaf(sc[t][j], scale, -base));
-          sum += p;
-          pf[t * 2 + (j >> 3)][j & 7] = static_cast<bf16>(p);
-        }
-      l = l * alpha + sum;
-      if (__any(alpha != 1.f)) {
+      for (int k = 0; k < AHEAD; ++k) kf[k] = k_frag(buf ^ 1, k);
+      const int s3 = block_slot(C, table, b + 3 < b1 ? b + 3 : e);
+      // The reference m of the weights is a whole number and moves only when the maximum outgrows
+      // it by 2^8: weights up to 256 cost no precision, and in most blocks nothing is rescaled.
+      const float want = ceilf(top * scale);
+      const bool grows = want > m + 8.f;
+      if (__any(grows)) {
+        const float alpha = grows ? exp2_f(m - want) : 1.f;
+        m = grows ? want : m;
+        l *= alpha;
 #pragma unroll
         for (int i = 0; i < DT; ++i) o[i] *= alpha;
       }
+      const float base = m == kNegInf ? 0.f : m;
+      uint32_t pw[4][4];  // weights, 4 x 8 bf16
+      constexpr int PAIRS = 16 / STEPS > 0 ? 16 / STEPS : 1;
+      __builtin_amdgcn_sched_barrier(0);
+      // K(b + 1) Q^T beside the softmax of b
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
+      for (int k = 0; k < STEPS; ++k) {
+        if (k + AHEAD < STEPS) kf[(k + AHEAD) % 3] = k_frag(buf ^ 1, k + AHEAD);
+        if (k + AHEAD >= STEPS) vf[k + AHEAD - STEPS] = v_frag(buf, k + AHEAD - STEPS);
+        sn[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k % 3], qf[k >> 1],
+                                                            k < 2 ? zero : sn[k & 1], 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bf16x8 vf = *reinterpret_cast<const bf16x8*>(
-              &lv[buf][(i * 32 + col) * VLD + u * 16 + hf * 8]);
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u], o[i], 0, 0, 0);
+        for (int e2 = k * PAIRS; e2 < (k + 1) * PAIRS; ++e2) {
+          const int t = e2 / 8, j = e2 % 8 * 2;
+          const float x = exp2_f(fmaf(sc[t][j], scale, -base));
+          const float y = exp2_f(fmaf(sc[t][j + 1], scale, -base));
+          l += x + y;
+          // one rounding of the weight to bf16 (at most 2^-8 of it), the matrix cores' type
+          pw[t * 2 + (j >> 3)][(j & 7) >> 1] =
+              __builtin_bit_cast(uint32_t, bf16x2{static_cast<bf16>(x), static_cast<bf16>(y)});
+          // (an empty statement that wants the pair here: it is not used before the branch below,
+          // and would be computed behind it)
+          asm volatile("" : "+v"(pw[t * 2 + (j >> 3)][(j & 7) >> 1]));
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      asm volatile("" : "+v"(l));
+      mask(sn, b + 1, s1);
+      bf16x8 pf[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        pf[u] = __builtin_bit_cast(bf16x8, make_uint4(pw[u][0], pw[u][1], pw[u][2], pw[u][3]));
+      // V(b)^T P(b)^T beside the next maximum and the staging of K(b + 2) and V(b + 1)
+      top = kNegInf;
+#pragma unroll
+      for (int v = 0; v < STEPS; ++v) {
+        if (v + AHEAD < STEPS) vf[(v + AHEAD) % 3] = v_frag(buf, v + AHEAD);
+        o[v % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[v % 3], pf[v / DT], o[v % DT], 0, 0, 0);
+        if (v < NC) put_k(buf, v);
+        if (v >= NC && v < 2 * NC) put_v(buf ^ 1, v - NC);
+        if (v == 2 * NC) {
+          fetch_k(s3);  // K(b + 3), or the last block once more, unused
+          fetch_v(s2);
+        }
+#pragma unroll
+        for (int j = v * 32 / STEPS; j < (v + 1) * 32 / STEPS; ++j) top = fmaxf(top, sn[j >> 4][j & 15]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      top = joined(top);
+      s0 = s1;
+      s1 = s2;
+      s2 = s3;
+      __syncthreads();
+    };
+    for (int b = b0; b < b1; ++b) {
+      iterate(sa, sb, b);
+      if (++b >= b1) break;
+      iterate(sb, sa, b);
     }
-    if (more) put(buf ^ 1);
-    slot = next;
-    next = after;
-    __syncthreads();
   }
 
   l += __shfl_xor(l, 32, 64);
@@ -513,50 +591,75 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int tiles_per_seq, Piece
       ml[0] = m;
       ml[1] = l;
     }
+    if (l == 0.f) return;  // (the merge does not read this piece)
     float* dst = W.o + ((long)piece * W.rows + out) * D + hf * 4;
-    if (l != 0.f) {
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<f4*>(dst + i * 32 + j * 8) =
-              f4{o[i][j * 4], o[i][j * 4 + 1], o[i][j * 4 + 2], o[i][j * 4 + 3]};
-    }
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f4*>(dst + i * 32 + j * 8) =
+            f4{o[i][j * 4], o[i][j * 4 + 1], o[i][j * 4 + 2], o[i][j * 4 + 3]};
   }
 }
 
 // ---------------------------------------------------------------- merge of the pieces
 
-// D / 4 lanes a row, pieces in order; a piece without keys (sum 0) left no output.
-template <int D>
+// D / 4 lanes hold a row; SG such groups share a row's pieces (piece p to group p % SG) and are
+// added in order. A piece without keys (sum 0) left no output.
+template <int D, int SG>
 __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArgs A, Pieces W) {
-  constexpr int LN = D / 4;
-  const long row = (long)blockIdx.x * (256 / LN) + threadIdx.x / LN;
-  const int l = threadIdx.x % LN;
-  if (row >= W.rows) return;
-  if (A.c.cu_seqlens != nullptr) {  // rows outside the sequences are left as they are
+  constexpr int LN = D / 4, RPB = 256 / LN / SG;
+  const int l = threadIdx.x % LN, grp = threadIdx.x / LN, sg = grp % SG;
+  const long row = (long)blockIdx.x * RPB + grp / SG;
+  bool mine = row < W.rows;
+  if (A.c.cu_seqlens != nullptr && mine) {  // rows outside the sequences are left as they are
     const long tok = row / A.Hq;
-    if (tok < clamped_offset(A.c.cu_seqlens, 0, A.c.T) ||
-        tok >= clamped_offset(A.c.cu_seqlens, A.c.N, A.c.T))
-      return;
+    mine = tok >= clamped_offset(A.c.cu_seqlens, 0, A.c.T) &&
+           tok < clamped_offset(A.c.cu_seqlens, A.c.N, A.c.T);
   }
+  const long at = mine ? row : 0;
   float top = kNegInf;
   for (int p = l; p < W.splits; p += LN) {
-    const float* ml = W.ml + ((long)p * W.rows + row) * 2;
+    const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)p * W.rows + at) * 2);
     if (ml[1] != 0.f) top = fmaxf(top, ml[0]);
   }
 #pragma unroll
   for (int k = 1; k < LN; k <<= 1) top = fmaxf(top, __shfl_xor(top, k, 64));
   f4 acc = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  for (int p = 0; p < W.splits; ++p) {
-    const float* ml = W.ml + ((long)p * W.rows + row) * 2;
-    const float lp = ml[1];
-    if (lp == 0.f) continue;
-    const float f = exp2_f(ml[0] - top);
-    sum += lp * f;
-    acc += *reinterpret_cast<const f4*>(W.o + ((long)p * W.rows + row) * D + l * 4) * f;
+  for (int base = 0; base < W.splits; base += LN) {
+    float f = 0.f, fl = 0.f;  // weight of piece base + l, and its share of the sum
+    if (base + l < W.splits) {
+      const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)(base + l) * W.rows + at) * 2);
+      if (ml[1] != 0.f) {
+        f = exp2_f(ml[0] - top);
+        fl = ml[1] * f;
+      }
+    }
+    const int n = W.splits - base < LN ? W.splits - base : LN;
+#pragma unroll 4
+    for (int j = sg; j < n; j += SG) {
+      const float fj = __shfl(f, j, LN), lj = __shfl(fl, j, LN);
+      const f4 x = *reinterpret_cast<const f4*>(W.o + ((long)(base + j) * W.rows + at) * D + l * 4);
+      sum += lj;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += lj == 0.f ? 0.f : x[i] * fj;
+    }
   }
+  if constexpr (SG > 1) {
+    __shared__ __align__(16) float red[256][4];
+    __shared__ float rs[256 / LN];
+    *reinterpret_cast<f4*>(red[threadIdx.x]) = acc;
+    if (l == 0) rs[grp] = sum;
+    __syncthreads();
+    if (sg != 0) return;
+#pragma unroll
+    for (int j = 1; j < SG; ++j) {
+      acc += *reinterpret_cast<const f4*>(red[threadIdx.x + j * LN]);
+      sum += rs[grp + j];
+    }
+  }
+  if (!mine) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<bf16x4*>((bf16*)A.o + row * D + l * 4) =
       bf16x4{static_cast<bf16>(acc[0] * inv), static_cast<bf16>(acc[1] * inv),
@@ -574,23 +677,36 @@ hipError_t run(const CacheAttnArgs& a, const CacheAttnPlan& p) {
   w.ml = w.o + (size_t)p.splits * w.rows * D;
   if (p.few_rows) {
     const dim3 grid((unsigned)((long)a.c.N * a.Hk * p.splits));
-    if (p.row_tiles == 1)
-      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1>), grid, dim3(256), 0, st, a,
+    if (p.row_tiles == 2)
+      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 2, 4>), grid, dim3(256), 0, st, a,
+                         p.split_blocks, w);
+    else if (p.waves == 8)
+      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 8>), grid, dim3(512), 0, st, a,
                          p.split_blocks, w);
     else
-      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 2>), grid, dim3(256), 0, st, a,
+      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 4>), grid, dim3(256), 0, st, a,
                          p.split_blocks, w);
   } else {
     const int units = a.c.cu_seqlens ? p.row_tiles : p.row_tiles * a.c.N;
-    hipLaunchKernelGGL((gdn2_cache_attn_tile_kernel<D>),
-                       dim3((unsigned)((long)units * a.Hk * p.splits)), dim3(256), 0, st, a,
-                       units, p.row_tiles, w);
+    const dim3 grid((unsigned)((long)units * a.Hk * p.splits));
+    if (D == 64 || p.tile_rows == 128)
+      hipLaunchKernelGGL((gdn2_cache_attn_tile_kernel<D, 4>), grid, dim3(256), 0, st, a, units,
+                         p.split_blocks, w);
+    else
+      hipLaunchKernelGGL((gdn2_cache_attn_tile_kernel<D, D == 64 ? 4 : 8>), grid, dim3(512), 0, st,
+                         a, units, p.split_blocks, w);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  constexpr int RPB = 256 / (D / 4);
-  hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D>), dim3((unsigned)((w.rows + RPB - 1) / RPB)),
-                     dim3(256), 0, st, a, w);
+  // Many pieces: a workgroup a row, or a row's chain of loads would be the call's latency
+  // (129 pieces of 256 rows: 44 us with one group a row).
+  constexpr int GR = 256 / (D / 4);
+  if (p.splits > 8)
+    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, GR>), dim3((unsigned)w.rows), dim3(256), 0,
+                       st, a, w);
+  else
+    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, 1>),
+                       dim3((unsigned)((w.rows + GR - 1) / GR)), dim3(256), 0, st, a, w);
   return hipGetLastError();
 }
 
@@ -609,21 +725,44 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
   // The lengths are on the device, so the cut goes by the table's width; pieces past a
   // sequence's end leave at once.
   p.few_rows = rows <= 32;
+  p.tile_rows = p.waves = 0;
   if (p.few_rows) {
     p.row_tiles = rows <= 16 ? 1 : 2;
-    long per = nb * N * Hk / 2048;  // about 8 workgroups a compute unit
+    const long groups = (long)N * Hk;
+    long per = nb * groups / 512;  // about two workgroups a compute unit
     if (per < nb / 256) per = nb / 256;
     per = (per + 3) / 4 * 4;  // a block a wave
     if (per < 4) per = 4;
+    p.waves = 4;
+    if (p.row_tiles == 1 && per < nb && (nb <= 8 || groups >= 256)) {
+      p.waves = 8;
+      per = nb;
+    }
     p.split_blocks = (int)per;
     p.splits = (int)((nb + per - 1) / per);
   } else {
-    p.row_tiles = packed ? (int)(rows / kTileRows + N) : (int)((rows + kTileRows - 1) / kTileRows);
-    p.split_blocks = 0;
-    const long wgs = (packed ? p.row_tiles : (long)p.row_tiles * N) * Hk;
-    long s = 512 / wgs;  // two workgroups a compute unit
-    if (s > (nb + 3) / 4) s = (nb + 3) / 4;
-    p.splits = s < 1 ? 1 : (int)s;
+    auto tiles = [&](int r) { return packed ? rows / r + N : (rows + r - 1) / r * N; };
+    const long wgs = tiles(128) * Hk;
+    // Pieces of the key axis where the tiles alone leave compute units idle: to one workgroup a
+    // unit, or two, by what was measured for d = 128: 1.1 us a block for a workgroup alone on its
+    // unit, 2.05 us for two; a merge of 5 us and 4 bytes a ps over its partial rows. (512 tokens
+    // behind 7680: 146 us in one piece, 54 in eight; 2048 tokens alone: 44 us in one, 52 in two.)
+    const double width = d / 128.0;
+    const auto cost = [&](long s) {
+      const double per = (double)((nb + s - 1) / s);
+      return width * (per * (wgs * s <= 256 ? 1.1 : 2.05) +
+                      (s > 1 ? 5.0 + 2.6e-4 * (double)(rows * (packed ? 1 : N) * Hk) * s : 0.0));
+    };
+    long best = 1;
+    for (const long s : {256 / wgs, 512 / wgs})
+      if (s > 1 && s <= 64 && nb / s >= 4 && cost(s) < cost(best)) best = s;
+    const long per = (nb + best - 1) / best;
+    // Eight waves on one staged copy of K and V where there are tiles enough: 265 against 290 us
+    // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512).
+    p.tile_rows = best == 1 && d == 128 && nb > 24 && tiles(256) * Hk >= 512 ? 256 : 128;
+    p.row_tiles = (int)(packed ? tiles(p.tile_rows) : tiles(p.tile_rows) / N);
+    p.split_blocks = (int)per;
+    p.splits = (int)((nb + per - 1) / per);
   }
   if (p.splits < 1) p.splits = 1;
   return p;

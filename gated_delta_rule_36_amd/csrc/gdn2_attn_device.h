@@ -23,6 +23,14 @@ __device__ __forceinline__ int wave_search(int N, long x, F key) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// A word that no one writes during the launch, at a wave-uniform address: a scalar load, which a
+// wave waits for apart from its vector loads (those return in order).
+template <typename T>
+__device__ __forceinline__ T scalar_load(const T* p, long i) {
+  typedef const __attribute__((address_space(4))) T* P;
+  return reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
 __device__ __forceinline__ int clamped_offset(const int* cu, int n, int T) {
   const int c = cu[n];
   return c < 0 ? 0 : c > T ? T : c;

@@ -72,6 +72,8 @@ struct CacheAttnArgs {
 struct CacheAttnPlan {
   bool few_rows;     // every wave holds all query rows of a (sequence, kv head)
   int row_tiles;     // few_rows: 16-row tiles; else: row tiles (per sequence, or in all)
+  int waves;         // few rows: waves of a workgroup
+  int tile_rows;     // many rows: query rows of a tile
   int splits;        // pieces of the key axis
   int split_blocks;  // few_rows: cache blocks per piece
 };

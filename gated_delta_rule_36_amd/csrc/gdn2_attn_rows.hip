@@ -24,7 +24,7 @@ namespace gdn2 {
 namespace {
 
 constexpr int kRowsPerLane = 4;  // rows in flight per lane group: 16 heads a wave at d = 128
-constexpr int kBwdGroups = 1024; // workgroups along the tokens in the backward
+constexpr int kBwdGroups = 512;  // workgroups along the tokens in the backward
 
 template <typename T> struct Piece4;
 template <> struct Piece4<bf16> {
@@ -328,9 +328,16 @@ gdn2_weight_grad_kernel(const float* partial, long rows_q, long rows_k, float* d
   const float* p = partial + (blockIdx.x == 0 ? 0 : rows_q * D);
   const long rows = blockIdx.x == 0 ? rows_q : rows_k;
   const int c = threadIdx.x & 15, j = threadIdx.x >> 4;
-  double acc = 0.0;
-  for (long r = j; r < rows; r += 64) acc += p[r * D + blockIdx.y * 16 + c];
-  red[j][c] = acc;
+  p += blockIdx.y * 16 + c;
+  double acc[4] = {};  // four loads in flight a thread: a chain of single ones is all latency
+  for (long r = j; r < rows; r += 256) {
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = r + i * 64 < rows ? p[(r + i * 64) * D] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += x[i];
+  }
+  red[j][c] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   __syncthreads();
   for (int half = 32; half > 0; half >>= 1) {
     if (j < half) red[j][c] += red[j + half][c];
@@ -430,8 +437,6 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
   const long first = start < 0 ? 0 : start;                 // position of the first new token
   const long blk = first / kCacheBlock + x;
   if (blk * kCacheBlock >= s.len || blk >= C.max_blocks) return;
-  const int slot = C.block_table[(long)n * C.max_blocks + blk];
-  if (slot < 0 || slot >= C.P) return;
   // new rows of this block: offsets [r0, r1)
   const int r0 = first > blk * kCacheBlock ? (int)(first - blk * kCacheBlock) : 0;
   const int r1 = s.len - blk * kCacheBlock < kCacheBlock ? (int)(s.len - blk * kCacheBlock)
@@ -439,14 +444,9 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
   if (r0 >= r1) return;  // no new token in it
   const long row_of = s.first + (blk * kCacheBlock - start);  // token row of offset 0
 
+  // The rows do not wait for the table: both loads go out together.
   const int tid = threadIdx.x, lane = tid & 63, grp = tid / LANES, l = tid % LANES;
   const Lane<D, IL> L(l, A.rot);
-  const long head = (long)slot * A.Hk + h;
-  uint8_t* kc = C.k + head * (kCacheBlock * D);
-  uint8_t* vc = C.v + head * (kCacheBlock * D);
-  const bool older = r0 > 0;  // older tokens in the block
-  const float ks_old = older ? C.k_scale[head] : 0.f, vs_old = older ? C.v_scale[head] : 0.f;
-
   Piece4<T> p0[PASSES], p1[PASSES];
   bf16x8 vr[PASSES];
   bool live[PASSES];
@@ -460,6 +460,14 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
     p1[u].load(kr + L.o1);
     vr[u] = *reinterpret_cast<const bf16x8*>((const T*)A.v + row * A.v_stride + (long)h * D + 8 * l);
   }
+  const int slot = C.block_table[(long)n * C.max_blocks + blk];
+  if (slot < 0 || slot >= C.P) return;
+  const long head = (long)slot * A.Hk + h;
+  uint8_t* kc = C.k + head * (kCacheBlock * D);
+  uint8_t* vc = C.v + head * (kCacheBlock * D);
+  const bool older = r0 > 0;  // older tokens in the block
+  const float ks_old = older ? C.k_scale[head] : 0.f, vs_old = older ? C.v_scale[head] : 0.f;
+
   double f[4];
   float wa[4], wb[4];
   lane_freq(L, A.inv_freq, f);
@@ -469,6 +477,8 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
   float kmax = 0.f, vmax = 0.f;
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
+    fine[u] = true;
+    if (!__any(live[u])) continue;  // a decoded token needs one pass of one wave
     float sn[4], cs[4];
     const double pos = static_cast<double>(blk * kCacheBlock + grp * PASSES + u);
 #pragma unroll
@@ -502,7 +512,12 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
     vmax = fmaxf(vmax, __shfl_xor(vmax, m, 64));
   }
   __shared__ float red[2][4];
-  __shared__ __align__(16) uint8_t vl[D][kCacheBlock + 16];
+  __shared__ __align__(16) uint8_t vl[D * kCacheBlock];
+  // Byte of (channel, column): the 16-byte chunk is swapped by the channel's octet, as the lanes
+  // of a row write channels 8 apart.
+  auto vplace = [](int ch, int col) {
+    return ch * kCacheBlock + ((((col >> 4) ^ (ch >> 3)) & 3) << 4) + (col & 15);
+  };
   if (lane == 0) {
     red[0][tid >> 6] = kmax;
     red[1][tid >> 6] = vmax;
@@ -526,6 +541,7 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
   uint32_t vcode[PASSES][2];
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
+    if (!__any(live[u])) continue;
     float f0[4], f1[4], v[8];
     from_pairs<IL>(ka[u], kb[u], f0, f1);
     // A key or value that is not finite marks its token: a key row of NaN, so that every query
@@ -574,20 +590,49 @@ __global__ void __launch_bounds__(256) gdn2_attn_prologue_kernel(AttnPrologueArg
       }
       o = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(&vl[c >> 2][(c & 3) * 16]) = o;
+    *reinterpret_cast<uint4*>(&vl[vplace(c >> 2, (c & 3) * 16)]) = o;
   }
   __syncthreads();
+  bool whole = true;
 #pragma unroll
-  for (int u = 0; u < PASSES; ++u)
-    if (live[u]) {
-      const int col = value_column(grp * PASSES + u);
+  for (int u = 0; u < PASSES; ++u) whole = whole && live[u];
+  if (whole) {
+    const int col = value_column(grp * PASSES);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        vl[8 * l + i][col] = (uint8_t)(vcode[u][i >> 2] >> (8 * (i & 3)));
+    for (int k = 0; k < 2; ++k) {  // channels 8 l + 4 k ..: a transpose of 4 x PASSES bytes
+      const uint32_t lo = __builtin_amdgcn_perm(vcode[1][k], vcode[0][k], 0x05010400u);
+      const uint32_t hi = __builtin_amdgcn_perm(vcode[1][k], vcode[0][k], 0x07030602u);
+      const int ch = 8 * l + 4 * k;
+      if constexpr (PASSES == 4) {
+        const uint32_t lo2 = __builtin_amdgcn_perm(vcode[3][k], vcode[2][k], 0x05010400u);
+        const uint32_t hi2 = __builtin_amdgcn_perm(vcode[3][k], vcode[2][k], 0x07030602u);
+        const uint32_t w[4] = {__builtin_amdgcn_perm(lo2, lo, 0x05040100u),
+                               __builtin_amdgcn_perm(lo2, lo, 0x07060302u),
+                               __builtin_amdgcn_perm(hi2, hi, 0x05040100u),
+                               __builtin_amdgcn_perm(hi2, hi, 0x07060302u)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(&vl[vplace(ch + i, col)]) = w[i];
+      } else {
+        const uint32_t w[4] = {lo, lo >> 16, hi, hi >> 16};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint16_t*>(&vl[vplace(ch + i, col)]) = (uint16_t)w[i];
+      }
     }
+  } else {
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u)
+      if (live[u]) {
+        const int col = value_column(grp * PASSES + u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          vl[vplace(8 * l + i, col)] = (uint8_t)(vcode[u][i >> 2] >> (8 * (i & 3)));
+      }
+  }
   __syncthreads();
   for (int c = tid; c < D * 4; c += 256)
-    reinterpret_cast<uint4*>(vc)[c] = *reinterpret_cast<const uint4*>(&vl[c >> 2][(c & 3) * 16]);
+    reinterpret_cast<uint4*>(vc)[c] =
+        *reinterpret_cast<const uint4*>(&vl[vplace(c >> 2, (c & 3) * 16)]);
 }
 
 // Units (sequence, touched cache block) and workgroups of query rows of the serving prologue.
