@@ -213,6 +213,7 @@ class _QKNormRope(torch.autograd.Function):
                                 norm)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
         eps, interleaved, norm = ctx.how

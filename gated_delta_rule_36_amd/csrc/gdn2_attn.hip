@@ -214,8 +214,7 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[q][t][i]);
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = max_rows(top);
       const float mn = fmaxf(m[q], top * scale);
       const float base = mn == kNegInf ? 0.f : mn;
       const float alpha = exp2_f(m[q] - base);
@@ -338,16 +337,15 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
   const int piece = blockIdx.x / A.Hk / units;
   const int unit = units - 1 - blockIdx.x / A.Hk % units;
   int n, tile;
+  SeqSpan s;
   if (C.cu_seqlens == nullptr) {
     n = unit % C.N;
     tile = unit / C.N;
-  } else {
-    n = wave_search(C.N, unit, [&](int i) {
-      return (long)clamped_offset(C.cu_seqlens, i, C.T) * G / ROWS + i;
-    });
-    tile = unit - (int)((long)clamped_offset(C.cu_seqlens, n, C.T) * G / ROWS) - n;
+    s = seq_span(C, n);
+  } else {  // sequence n owns the tiles from floor(first row / ROWS) + n on
+    n = packed_span(C, unit, s, [&](int first, int i) { return (long)first * G / ROWS + i; });
+    tile = unit - (int)((long)s.first * G / ROWS) - n;
   }
-  const SeqSpan s = seq_span(C, n);
   const long rows = (long)s.count * G;
   const long row0 = (long)tile * ROWS;
   if (tile < 0 || row0 >= rows) return;
@@ -478,18 +476,13 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
           }
       }
     };
-    auto joined = [&](float x) {  // maximum over the two lanes of a row
-      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x),
-                                                       false, false);
-      return fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
-    };
     mask(sa, b0, s0);
     float top = kNegInf;  // maximum of the block whose softmax is next
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = fmaxf(top, sa[t][j]);
-    top = joined(top);
+    top = max_halves(top);
     __syncthreads();
 
     // Block b: sc its scores, sn the place of the next one's. One product a step; the fences
@@ -559,7 +552,7 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
         for (int j = v * 32 / STEPS; j < (v + 1) * 32 / STEPS; ++j) top = fmaxf(top, sn[j >> 4][j & 15]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      top = joined(top);
+      top = max_halves(top);
       s0 = s1;
       s1 = s2;
       s2 = s3;

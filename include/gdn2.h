@@ -433,6 +433,8 @@ size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d
  *   seq_lens : device int32 [N]: tokens of every sequence, those of this call included. The
  *             new tokens of a sequence are its last ones; where it has fewer tokens than new
  *             rows, the leading rows hold no token (padding).
+ * Of a block that is read, all 64 value columns must hold finite values, also where no token is:
+ * a cache that starts as zeros and is written by gdn2_attn_prologue always does.
  * The new rows come as a fixed number T per sequence ([N, T, H, d]: cu_seqlens NULL, N = B) or
  * packed (cu_seqlens as for gdn2_chunk_fwd, B = 1).
  */
@@ -446,8 +448,8 @@ enum { GDN2_CACHE_BLOCK = 64 };
  *   new rows (then what the block held is dropped: its value positions without a token are
  *   cleared). Where a scale grows, the block's older codes are rescaled (exact, but for codes
  *   that fall below e4m3's normal range).
- *   A token whose key or value row holds a NaN or infinity (after norm and rotation) has a
- *   key row of NaN and a zero value row in the cache and does not count for the scales: every
+ *   A token whose key or value row holds a NaN, an infinity or a magnitude from 248 * 2^120 on
+ *   (after norm and rotation) has a key row of NaN and a zero value row in the cache and does not count for the scales: every
  *   query of that head which attends to it comes out NaN, others are not touched.
  *   q, k, v : rows as in gdn2_qk_norm_rope, strides of their own
  *   q_out   : dense [.., Hq, d]; zeros in rows without a token; may be q where that is dense

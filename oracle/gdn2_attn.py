@@ -10,6 +10,7 @@ from __future__ import annotations
 import numpy as np
 
 BLOCK = 64
+LARGEST = 248.0 * 2.0 ** 120  # from here on a code would stand for 2^128, an infinity
 
 
 def _split(n, rot, interleaved):
@@ -101,7 +102,7 @@ def append(cache, block_row, total, k, v):
         slot, o0, o1 = block_row[b], p0 - b * BLOCK, p1 - b * BLOCK
         for h in range(Hk):
             kn, vn = k[p0 - start:p1 - start, h], v[p0 - start:p1 - start, h]
-            fine = np.isfinite(kn).all(-1) & np.isfinite(vn).all(-1)
+            fine = (np.abs(kn) < LARGEST).all(-1) & (np.abs(vn) < LARGEST).all(-1)
             for held, scale, x, mark in ((cache.k, cache.k_scale, kn, np.nan),
                                          (cache.v, cache.v_scale, vn, 0.0)):
                 s = block_scale(np.abs(x[fine]).max() if fine.any() else 0.0)

@@ -177,6 +177,25 @@ def test_prologue_not_finite_tokens():
     assert np.isnan(paged.ref.k).any() and not np.isnan(paged.ref.v).any()
 
 
+def test_prologue_largest_and_smallest_values():
+    """Values near the ends of the range: bf16's largest (stored as a marked token), large ones
+    whose scale is 2^119, and ones below the smallest scale's codes."""
+    rng = np.random.default_rng(18)
+    Hq, Hk, d = 2, 2, 64
+    paged = Paged(rng, [40], Hk, d)
+
+    def spoil(x):
+        x[0, 3, Hq * d] = torch.finfo(BF).max
+        x[0, 7, (Hq + Hk) * d] = -torch.finfo(BF).max
+        x[0, 8, (Hq + Hk) * d] = 3.0e38
+        x[0, 9, (Hq + 1) * d: (Hq + 2) * d] *= 2.0 ** -80
+
+    say("attn_prologue largest values")
+    _prologue(rng, paged, [40], [40], Hq, False, 0, norm=False, spoil=spoil)
+    assert np.isnan(paged.ref.k[paged.table[0, 0], 0, [3, 7]]).all()
+    assert paged.ref.v_scale[paged.table[0, 0], 0] == 2.0 ** 120
+
+
 def test_prologue_leaves_other_blocks():
     rng = np.random.default_rng(9)
     lens = [100, 300]
@@ -320,6 +339,66 @@ def test_attention_long_context():
         _attention(rng, paged, [L] * 2, lens, 4, window=window)
 
 
+def _plain64(q, cache, table, lens, window=0):
+    """Attention in 64-bit torch on the device, [N, T, Hq, d] queries, and the sum of p |v|."""
+    import gated_delta_rule_36_amd as G
+    N, T, Hq, d = q.shape
+    Hk = cache.k.shape[1]
+    cols = G.value_columns("cuda")
+    out, spread = torch.empty(q.shape, dtype=torch.float64, device="cuda"), torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for n in range(N):
+        total = int(lens[n])
+        blocks = table[n, : -(-total // B64)].long()
+        k = (cache.k[blocks].double() * cache.k_scale[blocks].double()[..., None, None]).transpose(0, 1).reshape(Hk, -1, d)
+        v = (cache.v[blocks].float()[..., cols].double() * cache.v_scale[blocks].double()[..., None, None])
+        v = v.permute(1, 0, 3, 2).reshape(Hk, -1, d)
+        p = total - T + torch.arange(T, device="cuda")[:, None]
+        j = torch.arange(k.shape[1], device="cuda")
+        hide = (j > p) | ((j <= p - window) if window else (j < 0))
+        for h in range(Hq):
+            x = q[n, :, h].double() @ k[h // (Hq // Hk)].t().contiguous() / d ** 0.5
+            w = torch.softmax(x.masked_fill(hide, float("-inf")), -1)
+            out[n, :, h], spread[n, :, h] = w @ v[h // (Hq // Hk)], w @ v[h // (Hq // Hk)].abs()
+    return f64(out), f64(spread)
+
+
+@pytest.mark.parametrize("N,T,total,Hq,Hk,d,window", [
+    (16, 512, 1601, 16, 16, 128, 0),   # tiles of 256 rows, 8 waves
+    (8, 1000, 1900, 16, 16, 128, 1700),
+    (70, 1, 400, 8, 4, 128, 0),        # 280 (sequence, head) pairs: 8 waves, one piece
+    (70, 2, 1500, 8, 4, 64, 0),
+    (3, 1, 450, 4, 2, 64, 0),          # 8 blocks: a block a wave
+    (260, 3, 333, 4, 4, 64, 100),
+    (1, 40, 20000, 8, 2, 128, 0),      # a few tiles, the key axis cut many times
+])
+def test_attention_variants_at_size(N, T, total, Hq, Hk, d, window):
+    """Every way a call is cut, at the sizes that choose it, against 64-bit torch on the device."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(N + total)
+    say("cache_attention at size", N, T, total, Hq, Hk, d, window)
+    nb = -(-total // B64)
+    gen = torch.Generator(device="cuda").manual_seed(N + total)
+    P = N * nb
+    cache = G.kv_cache(P, Hk, d)
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        codes.view(torch.uint8).copy_(torch.randn(codes.shape, generator=gen, device="cuda").mul(50).clamp(-448, 448).to(
+            torch.float8_e4m3fn).view(torch.uint8))
+        scale.copy_(torch.exp2(torch.randint(-7, -4, scale.shape, generator=gen, device="cuda").float()))
+    table = torch.from_numpy(rng.permutation(P).astype(np.int32).reshape(N, nb)).cuda()
+    lens = rng.integers(max(T, total * 3 // 4), total + 1, N)
+    q = torch.randn(N, T, Hq, d, generator=gen, device="cuda").to(BF)
+    got = G.cache_attention(q, cache, table, _i32(lens), window=window)
+    torch.cuda.synchronize()
+    ref, spread = _plain64(q, cache, table, lens, window)
+    # the bound of attention_ref, with |k| at most 448 * 2^-5
+    qs = np.abs(f64(q)).sum(-1, keepdims=True)
+    A = qs * 448 * 2.0 ** -5 * d ** -0.5
+    hb = half(BF)
+    w = hb * hb if T * (Hq // Hk) <= 32 else hb
+    e = 2 * (d * U * A + 4 * U + 2 * U * A)
+    assert_within("o", got, ref, (e + w + 64 * U + U * total ** 0.5) * spread + hb * np.abs(ref) + 1e-38)
+
+
 def test_attention_offsets_past_32_bits():
     """Blocks past 2^31 bytes of a cache."""
     import gated_delta_rule_36_amd as G
@@ -426,6 +505,18 @@ def test_serving_step_captured():
         assert all(torch.equal(a, b) for a, b in zip(held, ref)), i
         for a, b in zip(paged.dev, twin):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_serving_many_packed_sequences():
+    """More sequences than one round of the search, in both kernels of a serving step."""
+    rng = np.random.default_rng(34)
+    new = [int(x) for x in rng.integers(0, 5, 90)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 150, 90))]
+    paged = Paged(rng, lens, 2, 64)
+    paged.fill(rng)
+    say("serving 90 packed sequences")
+    _prologue(rng, paged, new, lens, 4, True, 64, behind=2)
+    _attention(rng, paged, new, lens, 4, packed=True, behind=2)
 
 
 def test_two_streams():

@@ -192,6 +192,16 @@ def test_autograd_equals_the_calls():
     assert torch.equal(leaf.grad, one)
 
 
+def test_second_derivatives_are_refused():
+    import gated_delta_rule_36_amd as G
+    q, k, pos, w, rng = _case(15, 1, 3, 2, 2, 64, 64, "fp32")
+    fr = torch.from_numpy(inv_freq(64)).cuda()
+    q.requires_grad_()
+    (g,) = torch.autograd.grad(G.qk_norm_rope(q, k, fr)[0].sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.square().sum().backward()
+
+
 def test_capture_and_replay():
     """Forward and backward in one graph, replayed on new inputs."""
     import gated_delta_rule_36_amd as G
