@@ -346,28 +346,32 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
     n = packed_span(C, unit, s, [&](int first, int i) { return (long)first * G / ROWS + i; });
     tile = unit - (int)((long)s.first * G / ROWS) - n;
   }
-  const long rows = (long)s.count * G;
-  const long row0 = (long)tile * ROWS;
-  if (tile < 0 || row0 >= rows) return;
-  const long row_end = row0 + ROWS < rows ? row0 + ROWS : rows;
+  n = uniform(n);
+  tile = uniform(tile);
+  s = uniform(s);
+  const int rows = s.count * G;  // (at most tokens * Hq, which the host holds below 2^31)
+  if (tile < 0 || (long)tile * ROWS >= rows) return;
+  const int row0 = tile * ROWS;
+  const int row_last = rows - row0 > ROWS ? row0 + ROWS - 1 : rows - 1;
   const int p0 = s.len - s.count;  // position of the first query of the sequence
-  const int pmin = p0 + (int)(row0 / G), pmax = p0 + (int)((row_end - 1) / G);
+  const int pmin = p0 + row0 / G, pmax = p0 + row_last / G;
   const long span = (long)C.max_blocks * kCacheBlock;
   const int hi = pmax + 1 < span ? pmax + 1 : (int)span;
-  int b0 = (below_window(pmin, A.window) + 1) / kCacheBlock;
+  const int b0 = uniform((below_window(pmin, A.window) + 1) / kCacheBlock + piece * split_blocks);
   int b1 = hi > 0 ? (hi + kCacheBlock - 1) / kCacheBlock : 0;
-  b0 += piece * split_blocks;
-  if (b1 > b0 + split_blocks) b1 = b0 + split_blocks;
+  b1 = uniform(b1 > b0 + split_blocks ? b0 + split_blocks : b1);
 
-  const long wr0 = row0 + wave * 32;  // positions that this wave's rows span (uniform)
-  const long wr1 = wr0 + 32 < rows ? wr0 + 32 : rows;
-  const int wmin = wr0 < rows ? p0 + (int)(wr0 / G) : -1;
-  const int wmax = wr0 < rows ? p0 + (int)((wr1 - 1) / G) : -1;
-  const long r = wr0 + col;
+  // positions that this wave's rows span; a wave past the last row has none (-1)
+  const int wr0 = row0 + wave * 32;
+  const int wr1 = rows - wr0 > 32 ? wr0 + 31 : rows - 1;
+  const int wmin = uniform(wr0 < rows ? p0 + wr0 / G : -1);
+  const int wmax = uniform(wr0 < rows ? p0 + wr1 / G : -1);
+  const int r = wr0 + col;
   const bool live = r < rows;
-  const int pos = live ? p0 + (int)(r / G) : -1;
+  const int rt = (live ? r : 0) / G, rh = (live ? r : 0) % G;  // query token, head of the group
+  const int pos = live ? p0 + rt : -1;
   const int low = below_window(pos, A.window);
-  const long out = ((long)s.first + (live ? r / G : 0)) * A.Hq + h * G + (live ? r % G : 0);
+  const long out = ((long)s.first + rt) * A.Hq + h * G + rh;
   bf16x8 qf[QS];
   {
     const bf16* qr = (const bf16*)A.q + out * D + hf * 8;
@@ -457,6 +461,7 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
     fetch_v(s1);
     __syncthreads();
     const f16v zero = {};
+    const bf16 one = static_cast<bf16>(1.f);
     constexpr int AHEAD = 2;  // fragments are read two steps before their product
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
@@ -520,10 +525,12 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
           const int t = e2 / 8, j = e2 % 8 * 2;
           const float x = exp2_f(fmaf(sc[t][j], scale, -base));
           const float y = exp2_f(fmaf(sc[t][j + 1], scale, -base));
-          l += x + y;
-          // one rounding of the weight to bf16 (at most 2^-8 of it), the matrix cores' type
-          pw[t * 2 + (j >> 3)][(j & 7) >> 1] =
-              __builtin_bit_cast(uint32_t, bf16x2{static_cast<bf16>(x), static_cast<bf16>(y)});
+          // One rounding of the weight to bf16 (at most 2^-8 of it), the matrix cores' type. The
+          // sum is that of the rounded weights: what rounding takes from the numerator it then
+          // takes from the denominator, all of it where one key holds most of the weight.
+          const bf16x2 w2 = {static_cast<bf16>(x), static_cast<bf16>(y)};
+          l = __builtin_amdgcn_fdot2_f32_bf16(w2, bf16x2{one, one}, l, false);
+          pw[t * 2 + (j >> 3)][(j & 7) >> 1] = __builtin_bit_cast(uint32_t, w2);
           // (an empty statement that wants the pair here: it is not used before the branch below,
           // and would be computed behind it)
           asm volatile("" : "+v"(pw[t * 2 + (j >> 3)][(j & 7) >> 1]));

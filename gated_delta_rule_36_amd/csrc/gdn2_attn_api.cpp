@@ -192,7 +192,7 @@ int gdn2_cache_attention(const void* q, const void* k_cache, const void* v_cache
   if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16))
     return GDN2_INVALID_ARGUMENT;
   const long tokens = (long)B * T;
-  if (tokens * Hq > (long)INT_MAX) return GDN2_INVALID_ARGUMENT;
+  if (tokens * Hq > (long)INT_MAX - 1024) return GDN2_INVALID_ARGUMENT;  // rows, in whole tiles
   const gdn2::CacheAttnPlan p =
       gdn2::cache_attn_plan(cu_seqlens != nullptr, N, T, Hq, Hk, d, max_blocks, window);
   if (gdn2::cache_attn_groups(p, cu_seqlens != nullptr, N, Hk) > (long)INT_MAX)

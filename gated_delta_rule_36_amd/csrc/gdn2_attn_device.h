@@ -116,4 +116,11 @@ __device__ __forceinline__ int packed_span(const CacheView& c, long x, SeqSpan& 
   return n;
 }
 
+// The same value, known to be wave-uniform to the compiler, which loses sight of it where paths
+// join (bounds held in vector registers turn uniform branches into masked code).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ SeqSpan uniform(const SeqSpan& s) {
+  return SeqSpan{uniform(s.first), uniform(s.count), uniform(s.len)};
+}
+
 }  // namespace gdn2

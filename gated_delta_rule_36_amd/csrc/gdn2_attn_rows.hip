@@ -432,6 +432,9 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     x = unit - s.first / kCacheBlock - 2 * n;
     if (x < 0) return;
   }
+  n = uniform(n);
+  x = uniform(x);
+  s = uniform(s);
   const long start = s.len - s.count;                       // position of the first new row
   const long first = start < 0 ? 0 : start;                 // position of the first new token
   const long blk = first / kCacheBlock + x;
