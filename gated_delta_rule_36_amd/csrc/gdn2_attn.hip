@@ -729,12 +729,16 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
   if (p.few_rows) {
     p.row_tiles = rows <= 16 ? 1 : 2;
     const long groups = (long)N * Hk;
-    long per = nb * groups / 512;  // about two workgroups a compute unit
+    // A workgroup a compute unit: twice or half as many pieces cost 15 to 25% (4 sequences of 32 K
+    // tokens, 4 drafts, 16 heads on 2: 21.8 us; 25.0 with 512 workgroups, 27.5 with 128).
+    long per = nb * groups / 256;
     if (per < nb / 256) per = nb / 256;
     per = (per + 3) / 4 * 4;  // a block a wave
     if (per < 4) per = 4;
     p.waves = 4;
-    if (p.row_tiles == 1 && per < nb && (nb <= 8 || groups >= 256)) {
+    if (p.row_tiles == 1 && per < nb && nb <= 8) {
+      // up to a block a wave in one workgroup of 8: no merge (512 tokens: 7.2 against 7.9 us; 16
+      // blocks would take 10.3 against 9.0, a compute unit draws but 50 GB/s)
       p.waves = 8;
       per = nb;
     }
