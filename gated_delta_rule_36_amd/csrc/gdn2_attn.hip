@@ -761,8 +761,9 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
     for (const long s : {256 / wgs, 512 / wgs})
       if (s > 1 && s <= 64 && nb / s >= 4 && cost(s) < cost(best)) best = s;
     const long per = (nb + best - 1) / best;
-    // Eight waves on one staged copy of K and V where there are tiles enough: 265 against 290 us
-    // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512).
+    // Eight waves on one staged copy of K and V where there are tiles enough: 255 against 280 us
+    // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512),
+    // and 181 against 170 us at d = 64 (8192 tokens), where a block has half as much to stage.
     p.tile_rows = best == 1 && d == 128 && nb > 24 && tiles(256) * Hk >= 512 ? 256 : 128;
     p.row_tiles = (int)(packed ? tiles(p.tile_rows) : tiles(p.tile_rows) / N);
     p.split_blocks = (int)per;
