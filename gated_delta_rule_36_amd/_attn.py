@@ -276,8 +276,8 @@ def attn_prologue(q, k, v, cache, block_table, seq_lens, inv_freq, cu_seqlens=No
     [1, T, H, d] with cu_seqlens int32 [N + 1]; cache: a KVCache; block_table: int32
     [N, max_blocks], entries outside [0, P) naming no block; seq_lens: int32 [N], all tokens of
     each sequence with the new ones, which are its last. A sequence with fewer tokens than new
-    rows has its leading rows as padding (zeros in the result). Sequences must not share a block
-    that is written. out: optional contiguous result, which may be q.
+    rows has its leading rows as padding (zeros in the result). A block that is written must stand
+    in the table once. out: optional contiguous result, which may be q.
     Returns q_out, [.., Hq, d]."""
     B, T, Hq, Hk, d, N, P, MB, dev = _cache_args(q, cache, block_table, seq_lens, cu_seqlens)
     qs = _rows("q", q, (B, T, Hq, d), torch.bfloat16, dev)

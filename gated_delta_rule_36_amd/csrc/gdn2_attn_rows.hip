@@ -9,7 +9,7 @@
 // and its gradient, with dn the rotation of dy by -p f:
 //   dw = sum over rows of dn x r,  dx = r (w dn - x (r^2 / d) sum_c(w dn x))
 // Everything is fp32 from the load to the one rounding at the store; the angle is fp64 up to
-// the fraction of a turn, since p f reaches 10^6 turns where fp32 has lost the fraction.
+// the fraction of a quarter turn, since p f reaches 10^6 turns where fp32 has lost the fraction.
 //
 // All of it is bound by memory: each row is read once and written once. A row lies on d / 8
 // lanes, 8 channels a lane, so that every lane holds whole pairs and the rotation needs no
@@ -52,21 +52,22 @@ __device__ __forceinline__ void store4(float* p, const float* f) {
   else *reinterpret_cast<f4*>(p) = v;
 }
 
-// sin and cos of 2 pi t: t mod 1 and the quadrant in fp64, then the series on [-pi/4, pi/4]
-// (the first omitted terms are 1.8e-9 and 2.5e-8, below fp32's rounding).
-__device__ __forceinline__ void sincos_turns(double t, float& s, float& c) {
-  const double r = t - rint(t);
-  const double qd = rint(4.0 * r);
-  const float x = static_cast<float>(r - 0.25 * qd) * 6.28318530717958647692f;
+// sin and cos of t quarter turns: the nearest whole number leaves in the low bits of t + 1.5 * 2^52
+// (|t| < 2^51), the rest is exact in fp64; then the series on [-pi/4, pi/4] (the first omitted
+// terms are 1.8e-9 and 2.5e-8, below fp32's rounding).
+__device__ __forceinline__ void sincos_quarters(double t, float& s, float& c) {
+  const double magic = 6755399441055744.0;  // 1.5 * 2^52
+  const double w = t + magic;
+  const int q = (int)(uint32_t)__double_as_longlong(w);
+  const float x = static_cast<float>(t - (w - magic)) * 1.57079632679489661923f;
   const float y = x * x;
   const float sp =
       x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880))));
   const float cp = 1.f + y * (-0.5f + y * (1.f / 24 + y * (-1.f / 720 + y * (1.f / 40320))));
-  const int q = static_cast<int>(qd) & 3;
   s = (q & 1) ? cp : sp;
   c = (q & 1) ? sp : cp;
-  if (q == 2 || q == 3) s = -s;
-  if (q == 1 || q == 2) c = -c;
+  if (q & 2) s = -s;
+  if ((q + 1) & 2) c = -c;
 }
 
 // A lane's share of a row: offsets of its two 4-channel pieces, and its 4 pairs (a, b) in them.
@@ -107,13 +108,13 @@ __device__ __forceinline__ void from_pairs(const float* a, const float* b, float
   }
 }
 
-// The 4 frequencies of a lane in turns per position, 0 where it does not rotate (then the
+// The 4 frequencies of a lane in quarter turns per position, 0 where it does not rotate (then the
 // sines are 0 and the cosines 1).
 template <int D, bool IL>
 __device__ __forceinline__ void lane_freq(const Lane<D, IL>& L, const float* inv_freq, double* f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    f[i] = L.rotated ? static_cast<double>(inv_freq[L.pair + i]) * 0.15915494309189533577 : 0.0;
+    f[i] = L.rotated ? static_cast<double>(inv_freq[L.pair + i]) * 0.63661977236758134308 : 0.0;
 }
 
 template <bool IL, int D>
@@ -140,7 +141,7 @@ __device__ __forceinline__ void norm_rotate(float* a, float* b, const float* wa,
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) ss += a[i] * a[i] + b[i] * b[i];
-    r = 1.f / sqrtf(row_sum<LANES>(ss) * (1.f / D) + eps);
+    r = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + eps);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -175,7 +176,7 @@ __device__ __forceinline__ void token_rows(const T* x, T* y, int nh, const float
   long pos;
   if (!place(pos)) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sincos_turns(f[i] * static_cast<double>(pos), sn[i], cs[i]);
+  for (int i = 0; i < 4; ++i) sincos_quarters(f[i] * static_cast<double>(pos), sn[i], cs[i]);
 #pragma unroll
   for (int u = 0; u < kRowsPerLane; ++u) {
     if (u * RPW >= nh) break;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(256) gdn2_norm_rope_bwd_kernel(NormRopeArgs A)
     const long pos = A.positions ? A.positions[tok] : tok % A.T;
     float sn[4], cs[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sincos_turns(f[i] * static_cast<double>(pos), sn[i], cs[i]);
+    for (int i = 0; i < 4; ++i) sincos_quarters(f[i] * static_cast<double>(pos), sn[i], cs[i]);
 #pragma unroll
     for (int u = 0; u < kRowsPerLane; ++u) {
       if (u * RPW >= nh) break;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(256) gdn2_norm_rope_bwd_kernel(NormRopeArgs A)
       if (A.norm) {
         ss = row_sum<LANES>(ss);
         dot = row_sum<LANES>(dot);
-        r = 1.f / sqrtf(ss * (1.f / D) + A.eps);
+        r = rsqrtf(ss * (1.f / D) + A.eps);
         back = r * r * (1.f / D) * dot;
       }
       const int row = u * RPW + grp;
@@ -484,7 +485,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     float sn[4], cs[4];
     const double pos = static_cast<double>(blk * kCacheBlock + grp * PASSES + u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sincos_turns(f[i] * pos, sn[i], cs[i]);
+    for (int i = 0; i < 4; ++i) sincos_quarters(f[i] * pos, sn[i], cs[i]);
     to_pairs<IL>(p0[u], p1[u], ka[u], kb[u]);
     norm_rotate<LANES, D>(ka[u], kb[u], wa, wb, sn, cs, A.norm, A.eps);
     float km = 0.f, vm = 0.f;

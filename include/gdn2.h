@@ -383,7 +383,7 @@ enum {
  *     n = x / sqrt(mean(x^2) + eps) * weight
  *     pair i < rot / 2, angle = position * inv_freq[i]:
  *       y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin;   channels past rot: y = n
- * fp32 throughout, the angle reduced in fp64 (exact for any int32 position), one rounding.
+ * fp32 throughout, the angle reduced in fp64 (any int32 position), one rounding.
  *
  *   q, k               : [B, T, Hq, d], [B, T, Hk, d] (dtype). The rows of one token are dense;
  *                        token t (of B * T) starts at element t * q_stride / t * k_stride, so
@@ -453,7 +453,7 @@ enum { GDN2_CACHE_BLOCK = 64 };
  *   query of that head which attends to it comes out NaN, others are not touched.
  *   q, k, v : rows as in gdn2_qk_norm_rope, strides of their own
  *   q_out   : dense [.., Hq, d]; zeros in rows without a token; may be q where that is dense
- *   Two sequences must not have a block in common that this call writes.
+ *   A block that this call writes must stand in the table once.
  *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk. No tokens: a no-op.
  * Returns GDN2_OK or an error status.
  */

@@ -316,6 +316,19 @@ def test_attention_stale_bytes_behind_a_sequence(L):
     _attention(rng, paged, [L] * 2, lens, 3)
 
 
+def test_attention_shared_blocks():
+    """Sequences that share their first blocks, and one that names a block twice."""
+    rng = np.random.default_rng(41)
+    lens = [200, 200, 129]
+    paged = Paged(rng, lens, 2, 64)
+    paged.fill(rng)
+    paged.table[1, :2] = paged.table[0, :2]
+    paged.table[2, 1] = paged.table[2, 0]
+    say("cache_attention shared blocks")
+    for L in (1, 60):
+        _attention(rng, paged, [L] * 3, lens, 4)
+
+
 def test_attention_scales_far_apart():
     """Blocks whose scales differ by many powers of two, tiny and large scores."""
     rng = np.random.default_rng(21)

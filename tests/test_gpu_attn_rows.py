@@ -70,6 +70,24 @@ def test_forward(case):
         assert_within(name, y, ref, bound)
 
 
+def test_forward_frequencies_past_a_turn():
+    """Frequencies of several turns a position, negative ones, zero, at the ends of int32."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(16)
+    fr = (rng.standard_normal(32) * np.array([0.0, 1e-3, 1.0, 50.0] * 8)).astype(np.float32)
+    pos = np.array([[-2 ** 31, -2 ** 31 + 1, -1, 0, 1, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1]], np.int32)
+    q = draw(rng, 1, 8, 3, 64, dtype=torch.float32).cuda()
+    say("qk_norm_rope_fwd frequencies past a turn")
+    got, _ = G.qk_norm_rope_fwd(q, q, torch.from_numpy(fr).cuda(), positions=torch.from_numpy(pos).cuda())
+    torch.cuda.synchronize()
+    # the reference's own angle in 64 bits: the product of a 24-bit frequency and a 32-bit position
+    # needs 56 bits, so the largest angles (2^31 * 100 rad) are off by 2^-53 of them, 2.4e-5
+    ref, bound = rows_bound(f64(q), None, pos, fr, torch.float32, 1e-6, False, True)
+    size = np.abs(R.norm_rope(f64(q), None, pos, fr[:0]))
+    slack = 2.0 ** -52 * np.abs(pos[..., None].astype(np.float64)) * np.abs(fr).max()
+    assert_within("q", got, ref, bound + 2 * size.max(-1, keepdims=True) * slack[..., None])
+
+
 def test_forward_default_positions_and_in_place():
     import gated_delta_rule_36_amd as G
     q, k, _, w, _ = _case(8, 3, 20, 4, 2, 64, 64, "bf16")
