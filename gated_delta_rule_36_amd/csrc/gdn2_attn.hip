@@ -583,8 +583,9 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
   if (W.splits == 1) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     // The rows pass through the wave's own part of LDS (nobody reads tiles there any more) and
-    // leave in whole lines; stored as they lie, in pieces of 16 bytes, they cost 8192 tokens with a
-    // window of 512 on 8 heads 71 us instead of 64.5.
+    // leave in whole lines, past the caches, so that they are out before the kernel's end has to
+    // write the caches back (8192 tokens, window 512, 8 heads: 74 us as they lie, in pieces of 16
+    // bytes; 69 in lines; 66 in lines past the caches).
     constexpr int LR = D / 8, RP = 64 / LR;  // lanes of a row, rows of a pass
     bf16* const own = reinterpret_cast<bf16*>(&lds) + wave * 32 * KLD;
 #pragma unroll
@@ -603,7 +604,8 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
       const int r2 = p * RP + lane / LR, ch = lane % LR * 8;
       const long to = __shfl((int)out, r2, 64);
       const bf16x8 x = *reinterpret_cast<const bf16x8*>(own + r2 * KLD + ch);
-      if (wr0 + r2 < rows) *reinterpret_cast<bf16x8*>((bf16*)A.o + to * D + ch) = x;
+      if (wr0 + r2 < rows)
+        __builtin_nontemporal_store(x, reinterpret_cast<bf16x8*>((bf16*)A.o + to * D + ch));
     }
   } else if (live) {
     if (hf == 0) {
