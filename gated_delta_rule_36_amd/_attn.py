@@ -92,6 +92,10 @@ def _rows(name, t, shape, dtype, device):
     stride in elements."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _bad(name, t, shape, dtype, device)
+    return _token_stride(name, t, shape)
+
+
+def _token_stride(name, t, shape):
     B, T, H, d = shape
     if t.is_contiguous():
         return H * d
@@ -107,11 +111,9 @@ def _rows(name, t, shape, dtype, device):
     return st
 
 
-def _empty(t, stride):
-    """A contiguous tensor like t, whose tokens lie at `stride`."""
-    if stride == t.shape[2] * t.shape[3]:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
-    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _empty(t):
+    """A contiguous tensor like t. (A memory format costs the allocation half as much again.)"""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _rotation(inv_freq, d, dev):
@@ -136,7 +138,7 @@ def _norm_rope_args(q, k, inv_freq, positions, q_weight, k_weight):
     code = _CODES.get(dt)
     if code is None:
         raise TypeError(f"unsupported dtype {dt}; use bfloat16 or float32")
-    qs = _rows("q", q, shape, dt, dev)
+    qs = _token_stride("q", q, shape)
     ks = _rows("k", k, (B, T, Hk, d), dt, dev)
     if positions is not None:
         _dense("positions", positions, (B, T), torch.int32, dev)
@@ -165,7 +167,7 @@ def qk_norm_rope_fwd(q, k, inv_freq, positions=None, q_weight=None, k_weight=Non
     B, T, Hq, Hk, d, qs, ks, rot, code, dev, dt = _norm_rope_args(q, k, inv_freq, positions,
                                                                   q_weight, k_weight)
     if out is None:
-        qo, ko = _empty(q, qs), _empty(k, ks)
+        qo, ko = _empty(q), _empty(k)
     else:
         qo, ko = out
         _dense("out[0]", qo, (B, T, Hq, d), dt, dev)
@@ -190,13 +192,13 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq, positions=None, q_weight=No
     _dense("dq_out", dq_out, (B, T, Hq, d), dt, dev)
     _dense("dk_out", dk_out, (B, T, Hk, d), dt, dev)
     dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
-    make = torch.empty if B * T else torch.zeros
-    dwq = make(d, dtype=torch.float32, device=dev) if q_weight is not None else None
-    dwk = make(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+    make = torch.empty_like if B * T else torch.zeros_like
+    dwq = make(q_weight) if q_weight is not None else None
+    dwk = make(k_weight) if k_weight is not None else None
     ws, need = None, 0
     if dwq is not None or dwk is not None:
         need = _bwd_workspace(B, T, Hq, Hk, d)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = (dwk if dwq is None else dwq).new_empty((need + 3) // 4)
     _call("gdn2_qk_norm_rope_bwd", dev, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(),
           dk_out.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
           dq.data_ptr(), dk.data_ptr(), _p(dwq), _p(dwk), B, T, Hq, Hk, d, qs, ks, rot, eps,
@@ -280,7 +282,7 @@ def attn_prologue(q, k, v, cache, block_table, seq_lens, inv_freq, cu_seqlens=No
     in the table once. out: optional contiguous result, which may be q.
     Returns q_out, [.., Hq, d]."""
     B, T, Hq, Hk, d, N, P, MB, dev = _cache_args(q, cache, block_table, seq_lens, cu_seqlens)
-    qs = _rows("q", q, (B, T, Hq, d), torch.bfloat16, dev)
+    qs = _token_stride("q", q, q.shape)
     ks = _rows("k", k, (B, T, Hk, d), torch.bfloat16, dev)
     vs = _rows("v", v, (B, T, Hk, d), torch.bfloat16, dev)
     if q_weight is not None:
@@ -289,7 +291,7 @@ def attn_prologue(q, k, v, cache, block_table, seq_lens, inv_freq, cu_seqlens=No
         _dense("k_weight", k_weight, (d,), torch.float32, dev)
     rot = _rotation(inv_freq, d, dev)
     if out is None:
-        out = _empty(q, qs)
+        out = _empty(q)
     else:
         _dense("out", out, (B, T, Hq, d), torch.bfloat16, dev)
     kc, vc, kcs, vcs = cache
@@ -335,14 +337,16 @@ def cache_attention(q, cache, block_table, seq_lens, cu_seqlens=None, window=0, 
     need = _attention_workspace(cu_seqlens is not None, B, T, Hq, Hk, d, N, MB, window)
     if workspace is None:
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = seq_lens.new_empty((need + 3) // 4)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    else:
+        need = workspace.numel()
     kc, vc, ks, vs = cache
     _call("gdn2_cache_attention", dev, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
           vs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _p(cu_seqlens),
           out.data_ptr(), B, T, Hq, Hk, d, N, P, MB, window, scale, GDN2_BF16, _p(workspace),
-          0 if workspace is None else workspace.numel())
+          need)
     return out
 
 
