@@ -474,18 +474,25 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
     for (int k = 0; k < STEPS; ++k)
       sa[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(0, k), qf[k >> 1],
                                                           k < 2 ? zero : sa[k & 1], 0, 0, 0);
-    // Scores of block b that the masks leave; only blocks on the edge of some row's range need it.
+    // Scores of block b that the masks leave; only blocks on the edge of some row's range need it,
+    // and mostly of one end: each bound by itself is a compare with a constant and a select a score.
     auto mask = [&](f16v* x, int b, int slot) {
       const int key0 = b * kCacheBlock;
-      if (slot < 0 || key0 + kCacheBlock - 1 > wmin || key0 <= below_window(wmax, A.window)) {
-        const int last = slot < 0 ? -1 : pos;
+      if (slot < 0 || key0 + kCacheBlock - 1 > wmin) {
+        const int last = (slot < 0 ? -1 : pos - key0) - hf * 4;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int key = key0 + t * 32 + (j >> 2) * 8 + hf * 4 + (j & 3);
-            x[t][j] = (key > last) | (key <= low) ? kNegInf : x[t][j];
-          }
+          for (int j = 0; j < 16; ++j)
+            x[t][j] = t * 32 + (j >> 2) * 8 + (j & 3) > last ? kNegInf : x[t][j];
+      }
+      if (key0 <= below_window(wmax, A.window)) {
+        const int first = low - key0 - hf * 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            x[t][j] = t * 32 + (j >> 2) * 8 + (j & 3) <= first ? kNegInf : x[t][j];
       }
     };
     mask(sa, b0, s0);
