@@ -57,8 +57,10 @@ __device__ __forceinline__ int below_window(int p, int window) {
 struct Pieces {
   float* o;   // [splits][rows][D]
   float* ml;  // [splits][rows][2]
-  long rows;  // tokens * Hq
+  long rows;  // tokens * Hq; mixed batches, few rows: few for each (sequence, kv head)
   int splits;
+  int few;    // mixed batches: sequences of up to so many query rows a kv head go to the few-row
+              // kernel, the others to the many-row one; 0: one kernel has them all
 };
 
 // ---------------------------------------------------------------- few rows
@@ -82,6 +84,7 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
   const int e = piece * split_blocks + wave;
   const int early = A.window > 0 ? -1 : block_slot(C, table, e < C.max_blocks ? e : 0);
   const SeqSpan s = seq_span(C, n);
+  if (W.few && (long)s.count * G > W.few) return;
   const int rows = s.count * G < RT * 16 ? s.count * G : RT * 16;
   if (rows == 0) return;
   const int p0 = s.len - s.count;  // position of the first query
@@ -95,13 +98,14 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
   auto row_index = [&](int r) {  // row of the [tokens * Hq] output
     return ((long)s.first + r / G) * A.Hq + h * G + r % G;
   };
+  auto part_index = [&](int r) { return W.few ? (long)nh * W.few + r : row_index(r); };
   if (b0 >= b1) {  // nothing here: an empty piece (the only one: zeros)
     for (int r = threadIdx.x / 16; r < rows; r += NW * 4) {
       if (W.splits == 1) {
         for (int d = (threadIdx.x % 16) * 8; d < D; d += 128)
           *reinterpret_cast<uint4*>((bf16*)A.o + row_index(r) * D + d) = make_uint4(0, 0, 0, 0);
       } else if (threadIdx.x % 16 == 0) {
-        float* ml = W.ml + ((long)piece * W.rows + row_index(r)) * 2;
+        float* ml = W.ml + ((long)piece * W.rows + part_index(r)) * 2;
         ml[0] = kNegInf;
         ml[1] = 0.f;
       }
@@ -291,13 +295,13 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] += so[w][tr][ts * E + i];
     }
-    const long out = row_index(r);
     if (W.splits == 1) {
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      bf16* dst = (bf16*)A.o + out * D + ts * E;
+      bf16* dst = (bf16*)A.o + row_index(r) * D + ts * E;
 #pragma unroll
       for (int i = 0; i < E; ++i) dst[i] = static_cast<bf16>(x[i] * inv);
     } else {
+      const long out = part_index(r);
       float* dst = W.o + ((long)piece * W.rows + out) * D + ts * E;
 #pragma unroll
       for (int i = 0; i < E; ++i) dst[i] = x[i];
@@ -355,6 +359,11 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
   s = uniform(s);
   const int rows = s.count * G;  // (at most tokens * Hq, which the host holds below 2^31)
   if (tile < 0 || (long)tile * ROWS >= rows) return;
+  if (rows <= W.few) {  // the few-row kernel's (a tile at most): the merge leaves these rows alone
+    if (W.splits > 1 && piece == 0 && tid < rows)
+      W.ml[(((long)s.first + tid / G) * A.Hq + h * G + tid % G) * 2 + 1] = -1.f;
+    return;
+  }
   const int row0 = tile * ROWS;
   const int row_last = rows - row0 > ROWS ? row0 + ROWS - 1 : rows - 1;
   const int p0 = s.len - s.count;  // position of the first query of the sequence
@@ -634,22 +643,34 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
 // ---------------------------------------------------------------- merge of the pieces
 
 // D / 4 lanes hold a row; SG such groups share a row's pieces (piece p to group p % SG) and are
-// added in order. A piece without keys (sum 0) left no output.
-template <int D, int SG>
+// added in order. A piece without keys (sum 0) left no output. FEW: rows of the few-row kernel in a
+// mixed batch, `few` for each (sequence, kv head); else the rows of the output, but for those that
+// are marked as the few-row kernel's.
+template <int D, int SG, bool FEW>
 __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArgs A, Pieces W) {
   constexpr int LN = D / 4, RPB = 256 / LN / SG;
   const int l = threadIdx.x % LN, grp = threadIdx.x / LN, sg = grp % SG;
   const long row = (long)blockIdx.x * RPB + grp / SG;
-  bool mine = row < W.rows;
-  if (A.c.cu_seqlens != nullptr && mine) {  // rows outside the sequences are left as they are
+  long out = row;  // row of the output
+  if (row >= W.rows) return;  // (all lanes of a row, and with SG > 1 all of a workgroup)
+  if (FEW) {
+    const int r = (int)(row % W.few), G = A.Hq / A.Hk;
+    const long nh = row / W.few;
+    const int n = (int)(nh / A.Hk), h = (int)(nh % A.Hk);
+    const int first = clamped_offset(A.c.cu_seqlens, n, A.c.T);
+    const long rows = (long)(clamped_offset(A.c.cu_seqlens, n + 1, A.c.T) - first) * G;
+    if (r >= rows || rows > W.few) return;
+    out = ((long)first + r / G) * A.Hq + h * G + r % G;
+  } else if (A.c.cu_seqlens != nullptr) {  // rows outside the sequences stay as they are
     const long tok = row / A.Hq;
-    mine = tok >= clamped_offset(A.c.cu_seqlens, 0, A.c.T) &&
-           tok < clamped_offset(A.c.cu_seqlens, A.c.N, A.c.T);
+    if (tok < clamped_offset(A.c.cu_seqlens, 0, A.c.T) ||
+        tok >= clamped_offset(A.c.cu_seqlens, A.c.N, A.c.T) ||
+        (W.few && W.ml[row * 2 + 1] < 0.f))
+      return;
   }
-  const long at = mine ? row : 0;
   float top = kNegInf;
   for (int p = l; p < W.splits; p += LN) {
-    const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)p * W.rows + at) * 2);
+    const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)p * W.rows + row) * 2);
     if (ml[1] != 0.f) top = fmaxf(top, ml[0]);
   }
 #pragma unroll
@@ -659,7 +680,7 @@ __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArg
   for (int base = 0; base < W.splits; base += LN) {
     float f = 0.f, fl = 0.f;  // weight of piece base + l, and its share of the sum
     if (base + l < W.splits) {
-      const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)(base + l) * W.rows + at) * 2);
+      const f2v ml = *reinterpret_cast<const f2v*>(W.ml + ((long)(base + l) * W.rows + row) * 2);
       if (ml[1] != 0.f) {
         f = exp2_f(ml[0] - top);
         fl = ml[1] * f;
@@ -669,7 +690,7 @@ __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArg
 #pragma unroll 4
     for (int j = sg; j < n; j += SG) {
       const float fj = __shfl(f, j, LN), lj = __shfl(fl, j, LN);
-      const f4 x = *reinterpret_cast<const f4*>(W.o + ((long)(base + j) * W.rows + at) * D + l * 4);
+      const f4 x = *reinterpret_cast<const f4*>(W.o + ((long)(base + j) * W.rows + row) * D + l * 4);
       sum += lj;
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += lj == 0.f ? 0.f : x[i] * fj;
@@ -688,11 +709,38 @@ __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArg
       sum += rs[grp + j];
     }
   }
-  if (!mine) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<bf16x4*>((bf16*)A.o + row * D + l * 4) =
+  *reinterpret_cast<bf16x4*>((bf16*)A.o + out * D + l * 4) =
       bf16x4{static_cast<bf16>(acc[0] * inv), static_cast<bf16>(acc[1] * inv),
              static_cast<bf16>(acc[2] * inv), static_cast<bf16>(acc[3] * inv)};
+}
+
+template <int D>
+hipError_t run_few(const CacheAttnArgs& a, int row_tiles, int waves, int split_blocks, const Pieces& w) {
+  const hipStream_t st = (hipStream_t)a.stream;
+  const dim3 grid((unsigned)((long)a.c.N * a.Hk * w.splits));
+  if (row_tiles == 2)
+    hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 2, 4>), grid, dim3(256), 0, st, a, split_blocks, w);
+  else if (waves == 8)
+    hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 8>), grid, dim3(512), 0, st, a, split_blocks, w);
+  else
+    hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 4>), grid, dim3(256), 0, st, a, split_blocks, w);
+  return hipGetLastError();
+}
+
+template <int D, bool FEW>
+hipError_t run_merge(const CacheAttnArgs& a, const Pieces& w) {
+  const hipStream_t st = (hipStream_t)a.stream;
+  // Many pieces: a workgroup a row, or a row's chain of loads would be the call's latency
+  // (129 pieces of 256 rows: 44 us with one group a row).
+  constexpr int GR = 256 / (D / 4);
+  if (w.splits > 8)
+    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, GR, FEW>), dim3((unsigned)w.rows), dim3(256),
+                       0, st, a, w);
+  else
+    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, 1, FEW>),
+                       dim3((unsigned)((w.rows + GR - 1) / GR)), dim3(256), 0, st, a, w);
+  return hipGetLastError();
 }
 
 template <int D>
@@ -702,19 +750,12 @@ hipError_t run(const CacheAttnArgs& a, const CacheAttnPlan& p) {
   Pieces w;
   w.rows = tokens * a.Hq;
   w.splits = p.splits;
+  w.few = p.mixed_rows;
   w.o = (float*)a.workspace;
   w.ml = w.o + (size_t)p.splits * w.rows * D;
+  hipError_t e;
   if (p.few_rows) {
-    const dim3 grid((unsigned)((long)a.c.N * a.Hk * p.splits));
-    if (p.row_tiles == 2)
-      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 2, 4>), grid, dim3(256), 0, st, a,
-                         p.split_blocks, w);
-    else if (p.waves == 8)
-      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 8>), grid, dim3(512), 0, st, a,
-                         p.split_blocks, w);
-    else
-      hipLaunchKernelGGL((gdn2_cache_attn_rows_kernel<D, 1, 4>), grid, dim3(256), 0, st, a,
-                         p.split_blocks, w);
+    e = run_few<D>(a, p.row_tiles, p.waves, p.split_blocks, w);
   } else {
     const int units = a.c.cu_seqlens ? p.row_tiles : p.row_tiles * a.c.N;
     const dim3 grid((unsigned)((long)units * a.Hk * p.splits));
@@ -724,19 +765,17 @@ hipError_t run(const CacheAttnArgs& a, const CacheAttnPlan& p) {
     else
       hipLaunchKernelGGL((gdn2_cache_attn_tile_kernel<D, D == 64 ? 4 : 8>), grid, dim3(512), 0, st,
                          a, units, p.split_blocks, w);
+    e = hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  // Many pieces: a workgroup a row, or a row's chain of loads would be the call's latency
-  // (129 pieces of 256 rows: 44 us with one group a row).
-  constexpr int GR = 256 / (D / 4);
-  if (p.splits > 8)
-    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, GR>), dim3((unsigned)w.rows), dim3(256), 0,
-                       st, a, w);
-  else
-    hipLaunchKernelGGL((gdn2_cache_attn_merge_kernel<D, 1>),
-                       dim3((unsigned)((w.rows + GR - 1) / GR)), dim3(256), 0, st, a, w);
-  return hipGetLastError();
+  if (e == hipSuccess && p.splits > 1) e = run_merge<D, false>(a, w);
+  if (e != hipSuccess || p.mixed_rows == 0) return e;
+  if (p.splits > 1) w.o = w.ml + (size_t)p.splits * w.rows * 2;
+  w.rows = (long)a.c.N * a.Hk * p.mixed_rows;
+  w.splits = p.mixed_splits;
+  w.ml = w.o + (size_t)p.mixed_splits * w.rows * D;
+  e = run_few<D>(a, p.mixed_rows / 16, p.mixed_waves, p.mixed_blocks, w);
+  if (e == hipSuccess && p.mixed_splits > 1) e = run_merge<D, true>(a, w);
+  return e;
 }
 
 }  // namespace
@@ -745,18 +784,16 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
                               int window) {
   CacheAttnPlan p;
   const long G = Hq / Hk, rows = T * G;
-  // blocks that one call can reach: the table's, or what the window and the new tokens span
-  long nb = max_blocks;
-  if (window > 0) {
-    const long w = ((long)window + T + kCacheBlock - 3) / kCacheBlock + 1;
-    if (w < nb) nb = w;
-  }
-  // The lengths are on the device, so the cut goes by the table's width; pieces past a
-  // sequence's end leave at once.
-  p.few_rows = rows <= 32;
-  p.tile_rows = p.waves = 0;
-  if (p.few_rows) {
-    p.row_tiles = rows <= 16 ? 1 : 2;
+  // blocks that `tokens` new tokens of a sequence can reach: the table's, or what the window and
+  // the tokens span
+  const auto reach = [&](long tokens) {
+    const long w = ((long)window + tokens + kCacheBlock - 3) / kCacheBlock + 1;
+    return window > 0 && w < max_blocks ? w : (long)max_blocks;
+  };
+  const long nb = reach(T);
+  // The few-row kernel's pieces. The lengths are on the device, so the cut goes by the table's
+  // width; pieces past a sequence's end leave at once.
+  const auto cut = [&](long nb, int row_tiles, int& waves, int& split_blocks, int& splits) {
     const long groups = (long)N * Hk;
     // A workgroup a compute unit: twice or half as many pieces cost 15 to 25% (4 sequences of 32 K
     // tokens, 4 drafts, 16 heads on 2: 21.8 us; 25.0 with 512 workgroups, 27.5 with 128).
@@ -764,15 +801,25 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
     if (per < nb / 256) per = nb / 256;
     per = (per + 3) / 4 * 4;  // a block a wave
     if (per < 4) per = 4;
-    p.waves = 4;
-    if (p.row_tiles == 1 && per < nb && nb <= 8) {
+    waves = 4;
+    if (row_tiles == 1 && per < nb && nb <= 8) {
       // up to a block a wave in one workgroup of 8: no merge (512 tokens: 7.2 against 7.9 us; 16
       // blocks would take 10.3 against 9.0, a compute unit draws but 50 GB/s)
-      p.waves = 8;
+      waves = 8;
       per = nb;
     }
-    p.split_blocks = (int)per;
-    p.splits = (int)((nb + per - 1) / per);
+    split_blocks = (int)per;
+    splits = (int)((nb + per - 1) / per);
+    if (splits < 1) splits = 1;
+  };
+  p.few_rows = rows <= 32;
+  p.tile_rows = p.waves = 0;
+  p.mixed_rows = p.mixed_waves = p.mixed_blocks = 0;
+  p.mixed_splits = 1;
+  p.mixed_part_rows = 0;
+  if (p.few_rows) {
+    p.row_tiles = rows <= 16 ? 1 : 2;
+    cut(nb, p.row_tiles, p.waves, p.split_blocks, p.splits);
   } else {
     auto tiles = [&](int r) { return packed ? rows / r + N : (rows + r - 1) / r * N; };
     const long wgs = tiles(128) * Hk;
@@ -797,19 +844,37 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
     p.row_tiles = (int)(packed ? tiles(p.tile_rows) : tiles(p.tile_rows) / N);
     p.split_blocks = (int)per;
     p.splits = (int)((nb + per - 1) / per);
+    // Packed batches may hold single tokens and drafts beside prompts, and only the device knows
+    // which. A tile for one token walks its whole context alone, so sequences of few rows get a pass
+    // of the few-row kernel: 64 single tokens of 2 K to 4 K tokens, 16 heads on 4: 104 us as tiles,
+    // 38 with the pass; one over 32 K tokens beside a prompt of 2048: 670 and 61. It costs 3 us
+    // where all are prompts, and a tile of 32 blocks 35 us: so not below that, unless the
+    // sequences' tiles alone would fill the card (128 tokens over 1024 beside a prompt: 51 and 41).
+    if (packed && N > 1 && G <= 32) {
+      const int few = G <= 8 ? 16 : 32;
+      const long nf = reach(few / G);
+      if (nf >= 32 || (long)N * Hk >= 512) {
+        p.mixed_rows = few;
+        cut(nf, few / 16, p.mixed_waves, p.mixed_blocks, p.mixed_splits);
+        p.mixed_part_rows = (long)N * Hk * few;
+      }
+    }
   }
   if (p.splits < 1) p.splits = 1;
   return p;
 }
 
 size_t cache_attn_workspace_bytes(const CacheAttnPlan& p, long tokens, int Hq, int d) {
-  if (p.splits == 1) return 0;
-  return (size_t)p.splits * tokens * Hq * (d + 2) * sizeof(float);
+  size_t rows = 0;
+  if (p.splits > 1) rows += (size_t)p.splits * tokens * Hq;
+  if (p.mixed_splits > 1) rows += (size_t)p.mixed_splits * p.mixed_part_rows;
+  return rows * (d + 2) * sizeof(float);
 }
 
 long cache_attn_groups(const CacheAttnPlan& p, bool packed, int N, int Hk) {
   const long units = p.few_rows ? N : packed ? p.row_tiles : (long)p.row_tiles * N;
-  return units * Hk * p.splits;
+  const long tiles = units * Hk * p.splits, mixed = p.mixed_rows ? (long)N * Hk * p.mixed_splits : 0;
+  return tiles > mixed ? tiles : mixed;
 }
 
 hipError_t launch_cache_attn(const CacheAttnArgs& a, const CacheAttnPlan& p) {

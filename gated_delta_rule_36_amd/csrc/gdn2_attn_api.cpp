@@ -197,9 +197,8 @@ int gdn2_cache_attention(const void* q, const void* k_cache, const void* v_cache
       gdn2::cache_attn_plan(cu_seqlens != nullptr, N, T, Hq, Hk, d, max_blocks, window);
   if (gdn2::cache_attn_groups(p, cu_seqlens != nullptr, N, Hk) > (long)INT_MAX)
     return GDN2_INVALID_ARGUMENT;
-  if (p.splits > 1 && (workspace == nullptr ||
-                       workspace_bytes < gdn2::cache_attn_workspace_bytes(p, tokens, Hq, d)))
-    return GDN2_WORKSPACE_TOO_SMALL;
+  const size_t need = gdn2::cache_attn_workspace_bytes(p, tokens, Hq, d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
   gdn2::CacheAttnArgs a;
   a.q = q; a.o = o;
   a.c = view(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, T, N, P,

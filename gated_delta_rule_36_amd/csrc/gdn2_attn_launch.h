@@ -75,7 +75,11 @@ struct CacheAttnPlan {
   int waves;         // few rows: waves of a workgroup
   int tile_rows;     // many rows: query rows of a tile
   int splits;        // pieces of the key axis
-  int split_blocks;  // few_rows: cache blocks per piece
+  int split_blocks;  // cache blocks per piece
+  // Mixed batches: sequences of up to mixed_rows query rows a kv head (16 or 32; 0: no such pass)
+  // are left to a second pass of the few-row kernel, with a plan of its own.
+  int mixed_rows, mixed_waves, mixed_blocks, mixed_splits;
+  long mixed_part_rows;  // rows of its partial results
 };
 CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, int max_blocks,
                               int window);

@@ -114,6 +114,26 @@ def test_attention_refusals():
     assert ask(0, 1, 1, 16, 1, 128, 1, 1 << 20, 0) <= 260 * 16 * 130 * 4
 
 
+def test_mixed_batch_workspace():
+    """A packed batch over long tables needs room for its sequences of few rows as well: 16 pieces of
+    4 blocks, 16 rows for each of 8 x 2 (sequence, kv head)."""
+    ask = _lib.lib().gdn2_cache_attention_workspace_bytes
+    row = 130 * 4
+    need = ask(1, 1, 4000, 8, 2, 128, 8, 64, 0)
+    assert need == 16 * 8 * 2 * 16 * row
+    packed = dict(B=1, T=4000, Hq=8, N=8, MB=64, cu=F)
+    assert _serve(True, ws=None, **packed) == 3
+    assert _serve(True, wsz=need - 1, **packed) == 3
+    more = ask(1, 1, 200, 8, 2, 128, 8, 64, 0) - need   # a few tiles: the key axis of those as well
+    assert more > 0 and more % (200 * 8 * row) == 0
+    assert ask(1, 1, 4000, 8, 2, 128, 8, 64, 512) == 0   # ten blocks in reach: one pass
+    assert ask(1, 1, 4000, 8, 2, 128, 8, 16, 0) == 0
+    # rows of a group past 32: no sequence fits the few-row kernel
+    assert ask(1, 1, 4000, 80, 2, 128, 8, 64, 0) == 0
+    # many sequences: one piece each
+    assert ask(1, 1, 4000, 8, 2, 128, 256, 64, 0) == 0
+
+
 # ---------------------------------------------------------------- the binding
 
 @pytest.fixture

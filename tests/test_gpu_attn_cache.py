@@ -269,6 +269,29 @@ def test_attention_packed(new, lens, Hq, Hk, window):
     _attention(rng, paged, new, lens, Hq, packed=True, window=window, behind=5)
 
 
+@pytest.mark.parametrize("new,lens,Hq,Hk,d,width,window", [
+    ([1, 0, 200, 3, 4, 16, 5, 1], [300, 0, 900, 70, 4, 2600, 33, 0], 8, 2, 128, 50, 0),
+    ([2, 3, 1, 40], [700, 64, 2100, 40], 16, 1, 64, 40, 0),       # 32 rows, and 48
+    ([16, 17, 1, 60], [16, 17, 129, 1000], 2, 2, 128, 32, 0),     # 16 rows, and 17
+    ([1] * 40, [61 * i for i in range(40)], 4, 2, 128, 40, 0),    # single tokens alone
+    ([5, 100, 6, 1], [2500, 2500, 333, 2400], 6, 2, 64, 50, 2100),
+    ([1, 130, 1, 60], [3000, 500, 64, 2000], 8, 4, 128, 64, 0),   # both kernels cut the key axis
+    ([1, 50], [2200, 50], 32, 1, 128, 40, 0),                     # one token fills the rows
+    ([1, 2, 33], [100, 200, 300], 33, 1, 64, 40, 0),              # no token fits them
+    ([1] * 299 + [70], [i % 150 + 1 for i in range(299)] + [200], 6, 2, 64, 5, 50),  # short, but many
+])
+def test_attention_mixed_batches(new, lens, Hq, Hk, d, width, window):
+    """Packed batches over wide tables: sequences of few rows beside long ones, holes in a table."""
+    rng = np.random.default_rng(len(new) + Hq + window)
+    paged = Paged(rng, lens, Hk, d, table_width=width)
+    paged.fill(rng)
+    paged.table[0, 1] = -1
+    paged.table[-1, 2] = paged.P
+    say("cache_attention mixed", new, Hq, Hk, d, window)
+    for alias in (False, True):
+        _attention(rng, paged, new, lens, Hq, packed=True, window=window, behind=3, alias=alias)
+
+
 @pytest.mark.parametrize("L", [2, 90])
 def test_attention_padding_and_missing_blocks(L):
     """Padding rows, an empty sequence, holes in a table, a table too short for its sequence, a
