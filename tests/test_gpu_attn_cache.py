@@ -543,6 +543,39 @@ def test_serving_step_captured():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+def test_mixed_batch_captured():
+    """A packed call in a graph: which sequences hold single tokens changes between replays."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(35)
+    T, Hq, Hk, d = 200, 8, 2, 64
+    lens = [2100, 900, 64, 300, 0]
+    paged = Paged(rng, lens, Hk, d, table_width=40)
+    paged.fill(rng)
+    say("mixed batch captured")
+    q, out = draw(rng, 1, T, Hq, d).cuda(), torch.empty(1, T, Hq, d, dtype=torch.bfloat16, device="cuda")
+    cu, lt, tb = _i32([0, 1, 2, 66, 196, 196]), _i32(lens), paged.table_t()
+    call = lambda o: G.cache_attention(q, paged.dev, tb, lt, cu_seqlens=cu, out=o)
+    call(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    for i, new in enumerate([[1, 1, 64, 130, 0], [150, 4, 5, 1, 0], [1, 1, 1, 1, 0], [0, 160, 1, 39, 0],
+                             [1, 0, 0, 0, 0]]):
+        cu.copy_(_i32(np.concatenate([[0], np.cumsum(new)])))
+        q.copy_(draw(rng, 1, T, Hq, d))
+        out.fill_(5.0)
+        graph.replay()
+        ref = call(torch.full_like(out, 5.0))
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), i
+        assert (out[0, sum(new):] == 5.0).all()
+        spans = [(sum(new[:n]), c) for n, c in enumerate(new)]
+        exact, bound = attention_ref(f64(q).reshape(-1, Hq, d), paged, lens, spans, 0, None, few=False)
+        n = sum(new)
+        assert_within("o", f64(out).reshape(exact.shape)[:n], exact[:n], bound[:n])
+
+
 def test_serving_many_packed_sequences():
     """More sequences than one round of the search, in both kernels of a serving step."""
     rng = np.random.default_rng(34)
