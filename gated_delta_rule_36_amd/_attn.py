@@ -228,7 +228,9 @@ class _QKNormRope(torch.autograd.Function):
 def qk_norm_rope(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, eps=1e-6,
                  interleaved=False, norm=True):
     """Differentiable qk_norm_rope_fwd: gradients flow to q, k and the weights through the
-    library's backward. Positions and frequencies are constants."""
+    library's backward. Positions and frequencies are constants. (torch ties a leaf's accumulation
+    to the stream of its first use: before a backward pass is captured into a graph, drop eager
+    results of the same leaves that are still alive.)"""
     return _QKNormRope.apply(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, norm)
 
 
