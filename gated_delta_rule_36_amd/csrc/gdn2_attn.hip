@@ -834,8 +834,10 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
                       (s > 1 ? 5.0 + 2.6e-4 * (double)(rows * (packed ? 1 : N) * Hk) * s : 0.0));
     };
     long best = 1;
-    for (const long s : {256 / wgs, 512 / wgs})
-      if (s > 1 && s <= 64 && nb / s >= 4 && cost(s) < cost(best)) best = s;
+    for (long s : {256 / wgs, 512 / wgs}) {
+      if (s > nb / 4) s = nb / 4;  // (8 tokens over 32 K, 16 heads on 2: 624 us whole, 24 in pieces of 4)
+      if (s > 1 && cost(s) < cost(best)) best = s;
+    }
     const long per = (nb + best - 1) / best;
     // Eight waves on one staged copy of K and V where there are tiles enough: 255 against 280 us
     // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512),

@@ -134,6 +134,17 @@ def test_mixed_batch_workspace():
     assert ask(1, 1, 4000, 8, 2, 128, 256, 64, 0) == 0
 
 
+def test_few_tiles_over_a_long_context_are_cut():
+    """64 query rows a kv head make one tile: its key axis is cut however long it is, into pieces of
+    at least 4 blocks, and the room stays bounded."""
+    ask = _lib.lib().gdn2_cache_attention_workspace_bytes
+    row = 130 * 4
+    for blocks in (16, 65, 130, 512, 4096, 1 << 20):
+        need = ask(0, 1, 8, 16, 2, 128, 1, blocks, 0)
+        assert need > 0 and need % (8 * 16 * row) == 0, blocks
+        assert need // (8 * 16 * row) <= min(blocks // 4 + 1, 512), blocks
+
+
 # ---------------------------------------------------------------- the binding
 
 @pytest.fixture

@@ -406,6 +406,8 @@ def _plain64(q, cache, table, lens, window=0):
     (3, 1, 450, 4, 2, 64, 0),          # 8 blocks: a block a wave
     (260, 3, 333, 4, 4, 64, 100),
     (1, 40, 20000, 8, 2, 128, 0),      # a few tiles, the key axis cut many times
+    (1, 9, 20011, 16, 2, 128, 0),      # one tile a head: pieces of 4 blocks
+    (2, 35, 9000, 2, 2, 64, 0),
 ])
 def test_attention_variants_at_size(N, T, total, Hq, Hk, d, window):
     """Every way a call is cut, at the sizes that choose it, against 64-bit torch on the device."""
