@@ -822,30 +822,39 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
     cut(nb, p.row_tiles, p.waves, p.split_blocks, p.splits);
   } else {
     auto tiles = [&](int r) { return packed ? rows / r + N : (rows + r - 1) / r * N; };
+    // Pieces of the key axis where whole tiles would leave compute units idle, or one long tile would
+    // be the call's time. By what was measured in us a block (of the longest tile; c1: a workgroup
+    // alone on its unit, c2: two, unit: a unit's throughput), 5 us for the merge and 4 bytes a ps
+    // over its partial rows: 512 tokens behind 7680, 16 heads on 4: 146 us whole, 55 in eight; 8
+    // tokens over 32 K, 16 on 2: 624 and 24; 3000 tokens alone, 8 heads: 63 and 50 in two (d = 64: 50
+    // and 37); but 2048 tokens alone, 16 on 4: 41 and 50 in two.
+    const double c1 = d == 64 ? 0.92 : 1.25, c2 = d == 64 ? 1.31 : 2.0, unit = d == 64 ? 0.68 : 1.03;
     const long wgs = tiles(128) * Hk;
-    // Pieces of the key axis where the tiles alone leave compute units idle: to one workgroup a
-    // unit, or two, by what was measured for d = 128: 1.1 us a block for a workgroup alone on its
-    // unit, 2.05 us for two; a merge of 5 us and 4 bytes a ps over its partial rows. (512 tokens
-    // behind 7680: 146 us in one piece, 54 in eight; 2048 tokens alone: 44 us in one, 52 in two.)
-    const double width = d / 128.0;
+    // blocks of the longest tile, and of the mean one (prompts are causal)
+    const long most = reach(127 / G + 2 < T ? 127 / G + 2 : T);
+    const double own = (double)(packed ? T / N : T) / kCacheBlock;
+    const double mean = window > 0 ? (double)most : most - 0.5 * (own < most ? own : (double)most);
     const auto cost = [&](long s) {
-      const double per = (double)((nb + s - 1) / s);
-      return width * (per * (wgs * s <= 256 ? 1.1 : 2.05) +
-                      (s > 1 ? 5.0 + 2.6e-4 * (double)(rows * (packed ? 1 : N) * Hk) * s : 0.0));
+      const double per = (double)((most + s - 1) / s), work = (double)wgs * mean;
+      const double chain = per * ((double)wgs * s * mean / most <= 256.0 ? c1 : c2);
+      const double merge = s > 1 ? 5.0 + 2.0e-6 * d * (double)(rows * (packed ? 1 : N) * Hk) * s : 0.0;
+      return (chain > work * unit / 256 ? chain : work * unit / 256) + merge;
     };
     long best = 1;
-    for (long s : {256 / wgs, 512 / wgs}) {
-      if (s > nb / 4) s = nb / 4;  // (8 tokens over 32 K, 16 heads on 2: 624 us whole, 24 in pieces of 4)
+    // (Packed sequences differ in length, and the table's width says less of them: there only idle
+    // units are filled. 64 single tokens 46 us with two pieces for the tiles as well, 38 without.)
+    for (long s : {packed ? 1L : 2L, packed ? 1L : 3L, 256 / wgs, 512 / wgs}) {
+      if (s > most / 4) s = most / 4;
       if (s > 1 && cost(s) < cost(best)) best = s;
     }
-    const long per = (nb + best - 1) / best;
+    const long per = best == 1 ? nb : (most + best - 1) / best;
     // Eight waves on one staged copy of K and V where there are tiles enough: 255 against 280 us
     // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512),
     // and 181 against 170 us at d = 64 (8192 tokens), where a block has half as much to stage.
-    p.tile_rows = best == 1 && d == 128 && nb > 24 && tiles(256) * Hk >= 512 ? 256 : 128;
+    p.tile_rows = best == 1 && d == 128 && most > 24 && tiles(256) * Hk >= 512 ? 256 : 128;
     p.row_tiles = (int)(packed ? tiles(p.tile_rows) : tiles(p.tile_rows) / N);
     p.split_blocks = (int)per;
-    p.splits = (int)((nb + per - 1) / per);
+    p.splits = best == 1 ? 1 : (int)((most + per - 1) / per);
     // Packed batches may hold single tokens and drafts beside prompts, and only the device knows
     // which. A tile for one token walks its whole context alone, so sequences of few rows get a pass
     // of the few-row kernel: 64 single tokens of 2 K to 4 K tokens, 16 heads on 4: 104 us as tiles,

@@ -408,6 +408,9 @@ def _plain64(q, cache, table, lens, window=0):
     (1, 40, 20000, 8, 2, 128, 0),      # a few tiles, the key axis cut many times
     (1, 9, 20011, 16, 2, 128, 0),      # one tile a head: pieces of 4 blocks
     (2, 35, 9000, 2, 2, 64, 0),
+    (1, 700, 700, 4, 1, 64, 0),        # cut in pieces that the short tiles do not reach
+    (1, 500, 3001, 4, 2, 128, 1000),   # pieces of a window
+    (1, 1300, 1333, 8, 8, 128, 0),
 ])
 def test_attention_variants_at_size(N, T, total, Hq, Hk, d, window):
     """Every way a call is cut, at the sizes that choose it, against 64-bit torch on the device."""
