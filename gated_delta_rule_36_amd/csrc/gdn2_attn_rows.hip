@@ -387,17 +387,21 @@ __host__ __device__ constexpr int value_column(int t) {
 //
 // A (block, head) has one writer, so a growing scale needs no exchange with another workgroup.
 // Rows of a block are dealt so that a lane group holds 4 neighbouring tokens (2 at d = 64):
-// their codes of one value channel are neighbouring bytes of the block.
-template <int D, bool IL>
-__global__ void __launch_bounds__(256, 5)
+// their codes of one value channel are neighbouring bytes of the block. FEW: as many new tokens at
+// most as a wave has lane groups, and a wave a (block, head): a single token has work for 16 lanes,
+// and what bounds it is how many of these chains of loads are under way (one token of 256 sequences,
+// 4 heads: 10.0 us with four waves, 7.8 with one; of 512, 16 heads: 36.7 and 20.5).
+template <int D, bool IL, bool FEW>
+__global__ void __launch_bounds__(FEW ? 64 : 256, 5)
 gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) {
   typedef bf16 T;
-  constexpr int LANES = D / 8, PASSES = kCacheBlock / (256 / LANES);
+  constexpr int NT = FEW ? 64 : 256, NW = NT / 64;
+  constexpr int LANES = D / 8, PASSES = FEW ? 1 : kCacheBlock / (NT / LANES);
   const CacheView& C = A.c;
   if ((int)blockIdx.x >= kv_groups) {
     constexpr int CH = heads_per_wave<D>();
     const int chunks = (A.Hq + CH - 1) / CH;
-    const long item = (long)((int)blockIdx.x - kv_groups) * 4 + (threadIdx.x >> 6);
+    const long item = (long)((int)blockIdx.x - kv_groups) * NW + (threadIdx.x >> 6);
     const int tok = __builtin_amdgcn_readfirstlane((int)(item / chunks));
     const int tokens = C.cu_seqlens ? C.T : C.N * C.T;
     if (tok >= tokens) return;
@@ -451,9 +455,10 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   Piece4<T> p0[PASSES], p1[PASSES];
   bf16x8 vr[PASSES];
   bool live[PASSES];
+  const int own = FEW ? r0 + grp : grp * PASSES;  // first row of the lane group
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
-    const int r = grp * PASSES + u;
+    const int r = own + u;
     live[u] = r >= r0 && r < r1;
     const long row = row_of + (live[u] ? r : r0);
     const T* kr = (const T*)A.k + row * A.k_stride + (long)h * D;
@@ -481,7 +486,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     fine[u] = true;
     if (!__any(live[u])) continue;  // a decoded token needs one pass of one wave
     float sn[4], cs[4];
-    const double pos = static_cast<double>(blk * kCacheBlock + grp * PASSES + u);
+    const double pos = static_cast<double>(blk * kCacheBlock + own + u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sincos_quarters(f[i] * pos, sn[i], cs[i]);
     to_pairs<IL>(p0[u], p1[u], ka[u], kb[u]);
@@ -508,7 +513,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   }
   kmax = wave_max(kmax);
   vmax = wave_max(vmax);
-  __shared__ float red[2][4];
+  __shared__ float red[2][NW];
   __shared__ __align__(16) uint8_t vl[D * kCacheBlock];
   // Byte of (channel, column): the 16-byte chunk is swapped by the channel's octet, as the lanes
   // of a row write channels 8 apart.
@@ -520,8 +525,11 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     red[1][tid >> 6] = vmax;
   }
   __syncthreads();
-  kmax = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  vmax = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    kmax = fmaxf(kmax, red[0][w]);
+    vmax = fmaxf(vmax, red[1][w]);
+  }
   const float ks = fmaxf(ks_old, block_scale(kmax)), vs = fmaxf(vs_old, block_scale(vmax));
   if (tid == 0) {  // every thread has read the old scales (the barrier above)
     C.k_scale[head] = ks;
@@ -531,7 +539,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
 
   // keys: older rows follow a grown scale, new rows are written
   if (older && ks > ks_old)
-    for (int c = tid; c < r0 * (D / 16); c += 256) {
+    for (int c = tid; c < r0 * (D / 16); c += NT) {
       uint4* p = reinterpret_cast<uint4*>(kc) + c;
       *p = rescale_fp8(*p, ks_old * ki);
     }
@@ -549,7 +557,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     const uint32_t c1 =
         fine[u] ? pack_fp8(f1[0] * ki, f1[1] * ki, f1[2] * ki, f1[3] * ki) : 0x7f7f7f7fu;
     if (live[u]) {
-      uint8_t* kr = kc + (grp * PASSES + u) * D;
+      uint8_t* kr = kc + (own + u) * D;
       *reinterpret_cast<uint32_t*>(kr + L.o0) = c0;
       *reinterpret_cast<uint32_t*>(kr + L.o1) = c1;
     }
@@ -567,14 +575,14 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
 #pragma unroll
     for (int u = 0; u < PASSES; ++u)
       if (live[u]) {
-        const int col = value_column(grp * PASSES + u);
+        const int col = value_column(own + u);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           vc[(8 * l + i) * kCacheBlock + col] = (uint8_t)(vcode[u][i >> 2] >> (8 * (i & 3)));
       }
     return;
   }
-  for (int c = tid; c < D * 4; c += 256) {
+  for (int c = tid; c < D * 4; c += NT) {
     uint4 o = make_uint4(0, 0, 0, 0);
     if (older) o = reinterpret_cast<const uint4*>(vc)[c];
     if (vgrow) {  // the older tokens' codes, not what lies behind the last token
@@ -590,15 +598,15 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     *reinterpret_cast<uint4*>(&vl[vplace(c >> 2, (c & 3) * 16)]) = o;
   }
   __syncthreads();
-  bool whole = true;
+  bool whole = !FEW;
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) whole = whole && live[u];
   if (whole) {
-    const int col = value_column(grp * PASSES);
+    const int col = value_column(own);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {  // channels 8 l + 4 k ..: a transpose of 4 x PASSES bytes
-      const uint32_t lo = __builtin_amdgcn_perm(vcode[1][k], vcode[0][k], 0x05010400u);
-      const uint32_t hi = __builtin_amdgcn_perm(vcode[1][k], vcode[0][k], 0x07030602u);
+    for (int k = 0; k < 2 && !FEW; ++k) {  // channels 8 l + 4 k ..: a transpose of 4 x PASSES bytes
+      const uint32_t lo = __builtin_amdgcn_perm(vcode[PASSES > 1][k], vcode[0][k], 0x05010400u);
+      const uint32_t hi = __builtin_amdgcn_perm(vcode[PASSES > 1][k], vcode[0][k], 0x07030602u);
       const int ch = 8 * l + 4 * k;
       if constexpr (PASSES == 4) {
         const uint32_t lo2 = __builtin_amdgcn_perm(vcode[3][k], vcode[2][k], 0x05010400u);
@@ -620,20 +628,21 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
 #pragma unroll
     for (int u = 0; u < PASSES; ++u)
       if (live[u]) {
-        const int col = value_column(grp * PASSES + u);
+        const int col = value_column(own + u);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           vl[vplace(8 * l + i, col)] = (uint8_t)(vcode[u][i >> 2] >> (8 * (i & 3)));
       }
   }
   __syncthreads();
-  for (int c = tid; c < D * 4; c += 256)
+  for (int c = tid; c < D * 4; c += NT)
     __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(&vl[vplace(c >> 2, (c & 3) * 16)]),
                                 reinterpret_cast<u32x4*>(vc) + c);
 }
 
 // Units (sequence, touched cache block) and workgroups of query rows of the serving prologue.
 struct PrologueGrid {
+  bool few;  // one wave a (block, head)
   int per_seq;
   long units, q_groups;
 };
@@ -645,7 +654,9 @@ PrologueGrid prologue_grid(const AttnPrologueArgs& a) {
   // blocks that T tokens can touch: 1 for one token, up to two partial ones around whole ones
   g.per_seq = packed ? 0 : (int)(((long)a.c.T + kCacheBlock - 2) / kCacheBlock + 1);
   g.units = packed ? a.c.T / kCacheBlock + 2L * a.c.N : (long)a.c.N * g.per_seq;
-  g.q_groups = (tokens * ((a.Hq + CH - 1) / CH) + 3) / 4;
+  g.few = !packed && a.c.T <= 64 / (a.d / 8);
+  const long items = tokens * ((a.Hq + CH - 1) / CH);
+  g.q_groups = g.few ? items : (items + 3) / 4;
   return g;
 }
 
@@ -677,9 +688,14 @@ hipError_t run_norm_rope_bwd(const NormRopeArgs& a) {
 template <int D, bool IL>
 hipError_t run_prologue(const AttnPrologueArgs& a) {
   const PrologueGrid g = prologue_grid(a);
-  hipLaunchKernelGGL((gdn2_attn_prologue_kernel<D, IL>), dim3((unsigned)(g.units * a.Hk + g.q_groups)),
-                     dim3(256), 0, (hipStream_t)a.stream, a,
-                     (int)(g.units * a.Hk), g.per_seq);
+  const int kv_groups = (int)(g.units * a.Hk);
+  const dim3 grid((unsigned)(kv_groups + g.q_groups));
+  if (g.few)
+    hipLaunchKernelGGL((gdn2_attn_prologue_kernel<D, IL, true>), grid, dim3(64), 0,
+                       (hipStream_t)a.stream, a, kv_groups, g.per_seq);
+  else
+    hipLaunchKernelGGL((gdn2_attn_prologue_kernel<D, IL, false>), grid, dim3(256), 0,
+                       (hipStream_t)a.stream, a, kv_groups, g.per_seq);
   return hipGetLastError();
 }
 

@@ -120,6 +120,22 @@ def test_prologue_rows(new, lens, packed, d):
     _prologue(rng, paged, new, lens, 3, packed, d // 2, behind=4 if packed else 0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [2, 3, 4, 5, 8, 9])
+def test_prologue_few_tokens(T, d):
+    """Drafts: over a block's edge, in a new block, behind older ones, fewer tokens than rows, an empty
+    sequence, a missing block, values whose scales grow."""
+    rng = np.random.default_rng(T * 5 + d)
+    lens = [T, 64, 63 + T, 65, 127 + T // 2, 200, 1, 0, 40 + T, 130]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng)
+    paged.table[9, 2] = -1
+    say("attn_prologue few tokens", T, d)
+    _prologue(rng, paged, [T] * len(lens), lens, 4, False, d // 2, il=T % 2 == 0)
+    for size in (1e-2, 50.0):
+        _prologue(rng, paged, [T] * len(lens), lens, 4, False, d, norm=False, sizes=size)
+
+
 def test_prologue_many_sequences_packed():
     """More sequences than one round of the 64-way search, empty ones among them."""
     rng = np.random.default_rng(5)
