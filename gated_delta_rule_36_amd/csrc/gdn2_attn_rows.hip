@@ -447,6 +447,12 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   const int r1 = s.len - blk * kCacheBlock < kCacheBlock ? (int)(s.len - blk * kCacheBlock)
                                                          : kCacheBlock;
   if (r0 >= r1) return;  // no new token in it
+  // A block of few new tokens is one wave's also where the launch could not know it, in a packed
+  // batch: the others leave, whole waves that the barriers then do not wait for (512 single
+  // tokens, 16 heads: 62.8 and 38.0 us; prompts 1% slower).
+  const bool few = FEW || r1 - r0 <= 64 / LANES;
+  if (few && threadIdx.x >= 64) return;
+  const int nt = few ? 64 : NT;  // threads left
   const long row_of = s.first + (blk * kCacheBlock - start);  // token row of offset 0
 
   // The rows do not wait for the table: both loads go out together.
@@ -455,11 +461,11 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   Piece4<T> p0[PASSES], p1[PASSES];
   bf16x8 vr[PASSES];
   bool live[PASSES];
-  const int own = FEW ? r0 + grp : grp * PASSES;  // first row of the lane group
+  const int own = few ? r0 + grp : grp * PASSES;  // first row of the lane group
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
     const int r = own + u;
-    live[u] = r >= r0 && r < r1;
+    live[u] = r >= r0 && r < r1 && (u == 0 || !few);
     const long row = row_of + (live[u] ? r : r0);
     const T* kr = (const T*)A.k + row * A.k_stride + (long)h * D;
     p0[u].load(kr + L.o0);
@@ -526,7 +532,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
+  for (int w = 0; w < (few ? 1 : NW); ++w) {
     kmax = fmaxf(kmax, red[0][w]);
     vmax = fmaxf(vmax, red[1][w]);
   }
@@ -539,7 +545,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
 
   // keys: older rows follow a grown scale, new rows are written
   if (older && ks > ks_old)
-    for (int c = tid; c < r0 * (D / 16); c += NT) {
+    for (int c = tid; c < r0 * (D / 16); c += nt) {
       uint4* p = reinterpret_cast<uint4*>(kc) + c;
       *p = rescale_fp8(*p, ks_old * ki);
     }
@@ -582,7 +588,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
       }
     return;
   }
-  for (int c = tid; c < D * 4; c += NT) {
+  for (int c = tid; c < D * 4; c += nt) {
     uint4 o = make_uint4(0, 0, 0, 0);
     if (older) o = reinterpret_cast<const uint4*>(vc)[c];
     if (vgrow) {  // the older tokens' codes, not what lies behind the last token
@@ -598,7 +604,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
     *reinterpret_cast<uint4*>(&vl[vplace(c >> 2, (c & 3) * 16)]) = o;
   }
   __syncthreads();
-  bool whole = !FEW;
+  bool whole = !few;
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) whole = whole && live[u];
   if (whole) {
@@ -635,7 +641,7 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
       }
   }
   __syncthreads();
-  for (int c = tid; c < D * 4; c += NT)
+  for (int c = tid; c < D * 4; c += nt)
     __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(&vl[vplace(c >> 2, (c & 3) * 16)]),
                                 reinterpret_cast<u32x4*>(vc) + c);
 }
