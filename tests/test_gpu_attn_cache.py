@@ -136,6 +136,19 @@ def test_prologue_few_tokens(T, d):
         _prologue(rng, paged, [T] * len(lens), lens, 4, False, d, norm=False, sizes=size)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prologue_few_tokens_packed(d):
+    """Blocks of few and of many new tokens in one packed call, scales that grow and ones that do not."""
+    rng = np.random.default_rng(d + 1)
+    new = [1, 4, 5, 8, 9, 2, 70, 3, 0, 64]
+    lens = [64, 66, 5, 71, 200, 127, 134, 131, 0, 100]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng)
+    say("attn_prologue few tokens packed", d)
+    for size in (1.0, 1e-2, 50.0):
+        _prologue(rng, paged, new, lens, 4, True, d, norm=False, sizes=size, behind=2)
+
+
 def test_prologue_many_sequences_packed():
     """More sequences than one round of the 64-way search, empty ones among them."""
     rng = np.random.default_rng(5)
