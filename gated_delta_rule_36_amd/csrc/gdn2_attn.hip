@@ -49,6 +49,16 @@ __device__ __forceinline__ int block_slot(const CacheView& C, const int* table, 
   return (unsigned)s < (unsigned)C.P ? s : -1;
 }
 
+// 16 bytes of a value block of `bytes` bytes at `base` (wave-uniform), through a buffer whose size is
+// zero for a block that does not exist: it reads as zeros, since weights of zero would not keep a NaN
+// at `base` out of the product. (Its keys are those at `base`, masked by selection.) That costs
+// nothing; a branch around the loads took packed prompts with a window from 44.4 to 47.2 us and single
+// tokens with one from 51 to 52.
+__device__ __forceinline__ uint4 value_chunk(const uint8_t* base, int bytes, int off) {
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes, 0x00020000);
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 // Lowest key position that a query at position p sees, minus one.
 __device__ __forceinline__ int below_window(int p, int window) {
   return window > 0 && p >= window ? p - window : -1;
@@ -156,10 +166,10 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
   };
   auto load_v = [&](Block& r, int slot) {
     const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
-    const uint8_t* p = C.v + head * (kCacheBlock * D) + col * kCacheBlock + c * 16;
+    const uint8_t* p = C.v + head * (kCacheBlock * D);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
-      r.v[i] = *reinterpret_cast<const uint4*>(p + i * 16 * kCacheBlock);
+      r.v[i] = value_chunk(p, slot < 0 ? 0 : kCacheBlock * D, (i * 16 + col) * kCacheBlock + c * 16);
     r.vs = scalar_load(C.v_scale, head);
   };
 
@@ -242,10 +252,11 @@ gdn2_cache_attn_rows_kernel(CacheAttnArgs A, int split_blocks, Pieces W) {
         for (int i = 0; i < DT; ++i) o[q][i] *= alpha;
       }
     }
+    const float vs = slot < 0 ? 1.f : cur.vs;
 #pragma unroll
     for (int i = 0; i < DT; ++i) {
-      const bf16x8 v0 = codes_to_bf16(cur.v[i].x, cur.v[i].y, cur.vs);
-      const bf16x8 v1 = codes_to_bf16(cur.v[i].z, cur.v[i].w, cur.vs);
+      const bf16x8 v0 = codes_to_bf16(cur.v[i].x, cur.v[i].y, vs);
+      const bf16x8 v1 = codes_to_bf16(cur.v[i].z, cur.v[i].w, vs);
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         o[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[q][0], o[q][i], 0, 0, 0);
@@ -411,9 +422,10 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
   };
   auto fetch_v = [&](int slot) {
     const long head = (long)(slot < 0 ? 0 : slot) * A.Hk + h;
-    const uint4* p = reinterpret_cast<const uint4*>(C.v + head * (kCacheBlock * D));
+    const uint8_t* p = C.v + head * (kCacheBlock * D);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) vreg[j] = p[tid + j * NT];
+    for (int j = 0; j < NC; ++j)
+      vreg[j] = value_chunk(p, slot < 0 ? 0 : kCacheBlock * D, (tid + j * NT) * 16);
     vs = scalar_load(C.v_scale, head);
   };
   auto put_codes = [&](int buf, int j, const uint4& x, float scale_k) {
@@ -425,12 +437,13 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
   auto put_k = [&](int buf, int j) { put_codes(buf, j, kreg[j], ks); };
   // Value chunk cc holds the 4-token groups (t, cc), keys 16 t + 4 cc ..: they go where the lane
   // of half cc & 1 reads step t of the second product.
-  auto put_v = [&](int buf, int j) {
+  auto put_v = [&](int buf, int j, int slot) {
     const int i = tid + j * NT;
+    const float s = slot < 0 ? 1.f : vs;
     const int cc = i & 3;
     bf16* dv = &lds.v[buf][(i >> 2) * VLD + (cc & 1) * 8 + (cc >> 1) * 4];
-    const bf16x8 a = codes_to_bf16(vreg[j].x, vreg[j].y, vs);
-    const bf16x8 b = codes_to_bf16(vreg[j].z, vreg[j].w, vs);
+    const bf16x8 a = codes_to_bf16(vreg[j].x, vreg[j].y, s);
+    const bf16x8 b = codes_to_bf16(vreg[j].z, vreg[j].w, s);
     *reinterpret_cast<bf16x4*>(dv) = __builtin_shufflevector(a, a, 0, 1, 2, 3);
     *reinterpret_cast<bf16x4*>(dv + 16) = __builtin_shufflevector(a, a, 4, 5, 6, 7);
     *reinterpret_cast<bf16x4*>(dv + 32) = __builtin_shufflevector(b, b, 0, 1, 2, 3);
@@ -471,7 +484,7 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       put_k(1, j);
-      put_v(0, j);
+      put_v(0, j, s0);
     }
     fetch_k(s2);
     fetch_v(s1);
@@ -573,7 +586,7 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
         if (v + AHEAD < STEPS) vf[(v + AHEAD) % 3] = v_frag(buf, v + AHEAD);
         o[v % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[v % 3], pf[v / DT], o[v % DT], 0, 0, 0);
         if (v < NC) put_k(buf, v);
-        if (v >= NC && v < 2 * NC) put_v(buf ^ 1, v - NC);
+        if (v >= NC && v < 2 * NC) put_v(buf ^ 1, v - NC, s1);
         if (v == 2 * NC) {
           fetch_k(s3);  // K(b + 3), or the last block once more, unused
           fetch_v(s2);

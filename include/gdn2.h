@@ -429,7 +429,8 @@ size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d
  *   k_scale, v_scale : [P, Hk] fp32
  *   block_table : device int32 [N, max_blocks]: block b of sequence n holds its positions
  *             64 b .. 64 b + 63. An entry outside [0, P), or a position past the table, is a
- *             place that does not exist: nothing is written there and nothing is read.
+ *             place that does not exist: nothing is written there, and no query sees a key or
+ *             value there, whatever the pool holds elsewhere.
  *   seq_lens : device int32 [N]: tokens of every sequence, those of this call included. The
  *             new tokens of a sequence are its last ones; where it has fewer tokens than new
  *             rows, the leading rows hold no token (padding).

@@ -136,8 +136,8 @@ def attention(q, cache, block_row, total, window=0, scale=None):
         seen &= j > p[:, None] - window
     some = seen.any(1)
     for h in range(Hk):
-        k = (cache.k[slots, h] * cache.k_scale[slots, h][:, None, None]).reshape(-1, d)
-        v = (cache.v[slots, h] * cache.v_scale[slots, h][:, None, None]).reshape(-1, d)
+        k, v = (np.where(there[:, None, None], x[slots, h] * s[slots, h][:, None, None], 0.0).reshape(-1, d)
+                for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
         for g in range(h * (Hq // Hk), (h + 1) * (Hq // Hk)):
             with np.errstate(invalid="ignore"):
                 x = np.where(seen, np.where(seen, q[:, g] @ np.nan_to_num(k).T, 0) * scale, -np.inf)

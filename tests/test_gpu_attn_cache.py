@@ -337,6 +337,70 @@ def test_attention_padding_and_missing_blocks(L):
         _attention(rng, paged, [L] * 5, lens, 4, window=window)
 
 
+@pytest.mark.parametrize("N,L,total,Hq,Hk,d,window,packed", [
+    (2, 1, 500, 4, 2, 128, 0, False),       # few rows: 8 waves, one piece
+    (2, 1, 3000, 4, 2, 64, 0, False),       # pieces of the key axis
+    (2, 1, 500, 4, 2, 64, 130, False),
+    (2, 6, 500, 8, 2, 128, 0, False),       # two tiles of rows
+    (2, 90, 500, 4, 2, 128, 0, False),      # many rows
+    (2, 90, 500, 4, 2, 64, 200, False),
+    (1, 40, 5000, 4, 2, 128, 0, False),     # pieces of the key axis
+    (16, 512, 1601, 16, 16, 128, 0, False),  # 8 waves
+    (3, 70, 2500, 4, 2, 128, 0, True),      # single tokens beside a prompt
+])
+def test_attention_missing_blocks_read_nothing(N, L, total, Hq, Hk, d, window, packed):
+    """Holes in the table where no block of the pool but the sequences' own holds numbers: what they
+    do not name cannot show, so the rows are those over a pool of zeros."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(N + L)
+    say("cache_attention missing blocks read nothing", N, L, total, Hq, Hk, d, window, packed)
+    nb = -(-total // B64)
+    gen = torch.Generator(device="cuda").manual_seed(N + L)
+    P = N * nb + 2  # block 0 and the last one are no sequence's
+    cache = G.kv_cache(P, Hk, d)
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        codes[1:-1].view(torch.uint8).copy_(torch.randn(codes[1:-1].shape, generator=gen, device="cuda").mul(50).to(
+            torch.float8_e4m3fn).view(torch.uint8))
+        scale[1:-1] = 2.0 ** -6
+    table = 1 + rng.permutation(N * nb).astype(np.int32).reshape(N, nb)
+    for row in table:  # the first and the last block, a neighbour pair and every seventh
+        row[[0, 2, 3, nb - 1]] = [-1, P, 2 ** 31 - 1, -2 ** 31]
+        row[6::7] = -1
+    lens = np.full(N, total)
+    lens[0] -= 70
+    q = torch.randn(1 if packed else N, L, Hq, d, generator=gen, device="cuda").to(BF)
+    cu = _i32([0, 1, 2, L]) if packed else None
+    call = lambda: G.cache_attention(q, cache, _i32(table), _i32(lens), cu_seqlens=cu, window=window)
+    ref = call()
+    torch.cuda.synchronize()
+    assert ref.isfinite().all() and ref.any()
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        codes.view(torch.uint8)[[0, P - 1]] = 0x7f
+        scale[[0, P - 1]] = float("nan")
+    got = call()
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref)
+
+
+def test_attention_missing_blocks_in_an_unused_pool():
+    """The oracle's rows, with a first block of the pool that no one has written."""
+    rng = np.random.default_rng(51)
+    lens = [300, 128]
+    paged = Paged(rng, lens, 2, 128, spare=3)
+    paged.fill(rng)
+    unused = max(set(range(paged.P)) - set(paged.table[paged.table >= 0].tolist()))
+    paged.table[paged.table == 0] = unused
+    paged.table[0, 1] = -1
+    paged.table[1, 0] = paged.P
+    for x in (paged.ref.k, paged.ref.v, paged.ref.k_scale, paged.ref.v_scale):
+        x[0] = np.nan
+    paged.push()
+    say("cache_attention missing blocks, block 0 not written")
+    for L in (1, 10, 90):
+        for window in (0, 100):
+            _attention(rng, paged, [L] * 2, lens, 4, window=window)
+
+
 @pytest.mark.parametrize("L", [1, 6, 100])
 def test_attention_not_finite_keys(L):
     """A marked token makes NaN of the rows that see it, and of no others."""

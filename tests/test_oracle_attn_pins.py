@@ -126,3 +126,22 @@ def test_attention_equals_a_loop():
     assert not o.any()
     o, _ = R.attention(q, c, row, 3)  # two rows of padding
     assert not o[:2].any() and o[2:].any()
+
+
+def test_attention_over_missing_blocks_is_that_over_the_rest():
+    """Whatever the pool holds elsewhere."""
+    rng = np.random.default_rng(7)
+    c = R.Cache(4, 1, 8)
+    c.k[:], c.v[:] = rng.standard_normal(c.k.shape), rng.standard_normal(c.v.shape)
+    c.k_scale[:], c.v_scale[:] = 1.0, 1.0
+    for x in (c.k, c.v, c.k_scale, c.v_scale):
+        x[0] = np.nan
+    q = rng.standard_normal((2, 3, 8))
+    o, spread = R.attention(q, c, [3, -1, 1], 150)
+    for i in range(2):
+        keys = [j for j in range(149 + i) if j // 64 != 1]
+        kk, vv = (np.array([x[[3, -1, 1][j // 64], 0, j % 64] for j in keys]) for x in (c.k, c.v))
+        for h in range(3):
+            w = np.exp(kk @ q[i, h] * 8 ** -0.5)
+            assert np.allclose(o[i, h], w @ vv / w.sum(), atol=1e-12)
+    assert np.isfinite(spread).all()
