@@ -728,6 +728,12 @@ __global__ void __launch_bounds__(256) gdn2_cache_attn_merge_kernel(CacheAttnArg
              static_cast<bf16>(acc[2] * inv), static_cast<bf16>(acc[3] * inv)};
 }
 
+// Floats of one pass's partial results (`pieces` of each row: outputs, then maximum and sum), whole
+// 16-byte pieces: the next pass's, read as vectors, lie behind them.
+size_t partial_floats(int pieces, long rows, int d) {
+  return ((size_t)pieces * rows * (d + 2) + 3) / 4 * 4;
+}
+
 template <int D>
 hipError_t run_few(const CacheAttnArgs& a, int row_tiles, int waves, int split_blocks, const Pieces& w) {
   const hipStream_t st = (hipStream_t)a.stream;
@@ -782,7 +788,7 @@ hipError_t run(const CacheAttnArgs& a, const CacheAttnPlan& p) {
   }
   if (e == hipSuccess && p.splits > 1) e = run_merge<D, false>(a, w);
   if (e != hipSuccess || p.mixed_rows == 0) return e;
-  if (p.splits > 1) w.o = w.ml + (size_t)p.splits * w.rows * 2;
+  if (p.splits > 1) w.o += partial_floats(p.splits, w.rows, D);
   w.rows = (long)a.c.N * a.Hk * p.mixed_rows;
   w.splits = p.mixed_splits;
   w.ml = w.o + (size_t)p.mixed_splits * w.rows * D;
@@ -889,10 +895,10 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
 }
 
 size_t cache_attn_workspace_bytes(const CacheAttnPlan& p, long tokens, int Hq, int d) {
-  size_t rows = 0;
-  if (p.splits > 1) rows += (size_t)p.splits * tokens * Hq;
-  if (p.mixed_splits > 1) rows += (size_t)p.mixed_splits * p.mixed_part_rows;
-  return rows * (d + 2) * sizeof(float);
+  size_t floats = 0;
+  if (p.splits > 1) floats += partial_floats(p.splits, tokens * Hq, d);
+  if (p.mixed_splits > 1) floats += partial_floats(p.mixed_splits, p.mixed_part_rows, d);
+  return floats * sizeof(float);
 }
 
 long cache_attn_groups(const CacheAttnPlan& p, bool packed, int N, int Hk) {

@@ -134,6 +134,20 @@ def test_mixed_batch_workspace():
     assert ask(1, 1, 4000, 8, 2, 128, 256, 64, 0) == 0
 
 
+@pytest.mark.parametrize("T,Hq,Hk,d,N,blocks,pieces,few_pieces", [
+    (35, 1, 1, 128, 2, 143, 29, 36),
+    (101, 3, 3, 128, 3, 254, 51, 32),
+    (35, 1, 1, 64, 2, 143, 29, 36),
+])
+def test_mixed_batch_workspace_regions_are_aligned(T, Hq, Hk, d, N, blocks, pieces, few_pieces):
+    """The two passes' partial results lie one behind the other and are read 16 bytes at a time: the
+    second starts at a multiple of 16 bytes also where the first holds an odd number of rows."""
+    need = _lib.lib().gdn2_cache_attention_workspace_bytes(1, 1, T, Hq, Hk, d, N, blocks, 0)
+    row = (d + 2) * 4
+    first, second = pieces * T * Hq * row, few_pieces * N * Hk * 16 * row
+    assert first % 16 == 8 and need == first + 8 + second
+
+
 def test_few_tiles_over_a_long_context_are_cut():
     """64 query rows a kv head make one tile: its key axis is cut however long it is, into pieces of
     at least 4 blocks, and the room stays bounded."""

@@ -321,6 +321,32 @@ def test_attention_mixed_batches(new, lens, Hq, Hk, d, width, window):
         _attention(rng, paged, new, lens, Hq, packed=True, window=window, behind=3, alias=alias)
 
 
+@pytest.mark.parametrize("new,Hq,d,blocks", [([1, 33], 1, 128, 143), ([1, 34], 1, 64, 143), ([64, 2, 35], 3, 128, 254)])
+def test_attention_mixed_batches_with_odd_rows(new, Hq, d, blocks):
+    """Both passes with pieces of the key axis and an odd number of partial rows in the first, in a
+    workspace of just the size that was asked for."""
+    import gated_delta_rule_36_amd as G
+    rng = np.random.default_rng(blocks + d)
+    lens = [blocks * 64 - 5, 700, 9000][: len(new)]
+    T = 35 if len(new) == 2 else 101
+    paged = Paged(rng, lens, Hq, d, table_width=blocks)
+    paged.fill(rng)
+    say("cache_attention mixed, odd rows", new, Hq, d, blocks)
+    behind = T - sum(new)
+    spans, lead, cu = _layout(new, True, behind)
+    q = draw(rng, *lead, Hq, d)
+    need = G.cache_attention_workspace_bytes(1, T, Hq, Hq, d, len(new), blocks, packed=True)
+    room = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 7.0, device="cuda")
+    G.cache_attention(q.cuda(), paged.dev, paged.table_t(), _i32(lens), cu_seqlens=cu, out=out, workspace=room[:need])
+    torch.cuda.synchronize()
+    assert (room[need:] == 0x5a).all()
+    rows = f64(q).reshape(-1, Hq, d)
+    ref, bound = attention_ref(rows, paged, lens, spans)
+    ref[sum(new):] = 7.0
+    assert_within("o", f64(out).reshape(ref.shape), ref, bound)
+
+
 @pytest.mark.parametrize("L", [2, 90])
 def test_attention_padding_and_missing_blocks(L):
     """Padding rows, an empty sequence, holes in a table, a table too short for its sequence, a
