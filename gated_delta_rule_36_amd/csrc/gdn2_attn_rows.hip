@@ -591,13 +591,15 @@ gdn2_attn_prologue_kernel(AttnPrologueArgs A, int kv_groups, int units_per_seq) 
   for (int c = tid; c < D * 4; c += nt) {
     uint4 o = make_uint4(0, 0, 0, 0);
     if (older) o = reinterpret_cast<const uint4*>(vc)[c];
-    if (vgrow) {  // the older tokens' codes, not what lies behind the last token
+    if (vgrow) {  // the older tokens' codes, not what lies behind the last token (dropped drafts),
+                  // unless the scale is now the largest: a code there could stand for infinity
+      const uint32_t behind = vs < 0x1p120f ? ~0u : 0u;
       uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int left = r0 - (t * 16 + (c & 3) * 4);  // older tokens from this word's first on
         const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-        w[t] = (rescale_fp8(w[t], vs_old * vi) & keep) | (w[t] & ~keep);
+        w[t] = (rescale_fp8(w[t], vs_old * vi) & keep) | (w[t] & ~keep & behind);
       }
       o = make_uint4(w[0], w[1], w[2], w[3]);
     }

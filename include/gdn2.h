@@ -448,10 +448,12 @@ enum { GDN2_CACHE_BLOCK = 64 };
  *   rows in it, and not below its scale so far unless the block's first position is among the
  *   new rows (then what the block held is dropped: its value positions without a token are
  *   cleared). Where a scale grows, the block's older codes are rescaled (exact, but for codes
- *   that fall below e4m3's normal range).
+ *   that fall below e4m3's normal range). What lies behind the new tokens (dropped drafts) stays,
+ *   except that values there are cleared where their scale grows to 2^120, the largest.
  *   A token whose key or value row holds a NaN, an infinity or a magnitude from 248 * 2^120 on
- *   (after norm and rotation) has a key row of NaN and a zero value row in the cache and does not count for the scales: every
- *   query of that head which attends to it comes out NaN, others are not touched.
+ *   (after norm and rotation) has a key row of NaN and a zero value row in the cache and does
+ *   not count for the scales: every query of that head which attends to it comes out NaN, others
+ *   are not touched.
  *   q, k, v : rows as in gdn2_qk_norm_rope, strides of their own
  *   q_out   : dense [.., Hq, d]; zeros in rows without a token; may be q where that is dense
  *   A block that this call writes must stand in the table once.

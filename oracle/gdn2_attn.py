@@ -110,6 +110,8 @@ def append(cache, block_row, total, k, v):
                     old = scale[slot, h]
                     s = max(s, old)
                     held[slot, h, :o0] = round_e4m3(held[slot, h, :o0] * (old / s))
+                    if held is cache.v and s > old and s >= 2.0 ** 120:
+                        held[slot, h, o1:] = 0.0
                 elif held is cache.v:
                     held[slot, h, o1:] = 0.0
                 scale[slot, h] = s

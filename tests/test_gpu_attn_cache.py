@@ -225,6 +225,31 @@ def test_prologue_largest_and_smallest_values():
     assert paged.ref.v_scale[paged.table[0, 0], 0] == 2.0 ** 120
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kept", [30, 1, 60])
+def test_prologue_scale_grows_before_dropped_drafts(kept, d):
+    """Drafts are dropped and the next token's values raise the block's scale to its largest: what the
+    drafts left behind it must not stand for infinities, which weights of zero do not mask."""
+    rng = np.random.default_rng(kept + d)
+    Hq, Hk = 4, 2
+    paged = Paged(rng, [64], Hk, d)
+    first = (Hq + Hk) * d  # of the values
+
+    def drafts(x):
+        x[0, kept:, first:] = 448.0
+
+    def large(x):
+        x[0, 0, first:] = 3.0e38
+
+    say("attn_prologue scale grows before dropped drafts", kept, d)
+    _prologue(rng, paged, [kept + 3], [kept + 3], Hq, False, d, spoil=drafts)
+    assert paged.ref.v_scale[paged.table[0, 0], 0] == 1.0
+    _prologue(rng, paged, [1], [kept + 1], Hq, False, d, spoil=large)
+    assert paged.ref.v_scale[paged.table[0, 0], 0] == 2.0 ** 120
+    out = _attention(rng, paged, [1], [kept + 1], Hq, q=draw(rng, 1, 1, Hq, d, scale=0.1))
+    assert out.isfinite().all()
+
+
 def test_prologue_leaves_other_blocks():
     rng = np.random.default_rng(9)
     lens = [100, 300]

@@ -107,6 +107,22 @@ def test_append_piecewise_equals_at_once_where_scales_stay():
     assert np.abs(grown - k[64:100, 0]).max() <= 10 * 2 ** -4 + parts.k_scale[0, 0] * 2 ** -9
 
 
+def test_append_clears_values_behind_the_largest_scale():
+    """What lies behind the new tokens stays, whatever the scales do, except for values whose scale
+    grows to 2^120."""
+    c = R.Cache(1, 1, 8)
+    one = lambda x: np.full((1, 1, 8), x)
+    R.append(c, [0], 5, np.ones((5, 1, 8)), np.ones((5, 1, 8)))
+    R.append(c, [0], 3, one(1.0), one(1e4))
+    held = c.v[0, 0] * c.v_scale[0, 0]
+    assert (held[:2] == 1).all() and (np.abs(held[2] - 1e4) <= 1e4 / 16).all() and (c.v[0, 0, 3:5] > 0).all()
+    R.append(c, [0], 3, one(1.0), one(448 * 2.0 ** 119))
+    assert c.v_scale[0, 0] == 2.0 ** 119 and (c.v[0, 0, 3:5] > 0).all()
+    R.append(c, [0], 3, one(1.0), one(240 * 2.0 ** 120))
+    assert c.v_scale[0, 0] == 2.0 ** 120 and (c.v[0, 0, 2] == 240).all() and not c.v[0, 0, 3:].any()
+    assert (c.k[0, 0, 3:5] > 0).all()
+
+
 def test_attention_equals_a_loop():
     rng = np.random.default_rng(6)
     c = R.Cache(4, 2, 8)
