@@ -14,7 +14,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import GDN2_BF16, GDN2_F32, Gdn2Error, lib
+from ._lib import GDN2_BF16, GDN2_F32, Gdn2Error, _aligned_gradient, lib
 
 CACHE_BLOCK = 64  # tokens per cache block
 _INTERLEAVED, _NO_NORM = 1, 2
@@ -219,7 +219,7 @@ class _QKNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
         eps, interleaved, norm = ctx.how
-        dq_out, dk_out = dq_out.contiguous(), dk_out.contiguous()
+        dq_out, dk_out = _aligned_gradient(dq_out), _aligned_gradient(dk_out)
         dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq, positions, q_weight,
                                             k_weight, eps, interleaved, norm)
         return dq, dk, dwq, dwk, None, None, None, None, None

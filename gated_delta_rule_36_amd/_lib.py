@@ -482,6 +482,13 @@ def block_epilogue(o, gate, weight, out=None):
     return y
 
 
+def _aligned_gradient(t):
+    """A gradient as autograd hands it over (a view of any layout, at any offset) as the kernels
+    read it: contiguous, at a multiple of 16 bytes."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _GatedDeltaRule2(torch.autograd.Function):
     """Autograd wrapper: the training forward keeps the backward's intermediates; the
     backward consumes them (bf16)."""
@@ -498,8 +505,8 @@ class _GatedDeltaRule2(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, dsN):
         q, k, v, g, b, w, s0, cu = ctx.saved_tensors
-        do = do.contiguous() if do is not None else torch.zeros_like(v)
-        dsN = None if dsN is None else dsN.contiguous()
+        do = _aligned_gradient(do) if do is not None else torch.zeros_like(v)
+        dsN = None if dsN is None else _aligned_gradient(dsN)
         dq, dk, dv, dg, db, dw, ds0 = chunk_bwd(q, k, v, g, b, w, do, initial_state=s0,
                                                 d_final_state=dsN, cu_seqlens=cu,
                                                 saved=ctx.saved)

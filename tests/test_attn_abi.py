@@ -219,6 +219,60 @@ def test_norm_rope_binding_refusals(anywhere):
         G.qk_norm_rope_bwd(q, k, q, k.float(), fr)
 
 
+@pytest.mark.parametrize("shift", [0, 3, 5])
+def test_gradients_at_any_offset(monkeypatch, shift):
+    """Autograd's gradients may be views that start anywhere (here behind `shift` elements of one flat
+    tensor): the entry point gets them contiguous and aligned, with their values."""
+    import gated_delta_rule_36_amd as G
+    seen = []
+    monkeypatch.setattr(_attn, "_need_gpu", lambda t: None)
+    monkeypatch.setattr(_attn, "_call", lambda name, dev, *a: seen.append((name, a)))
+    q = torch.zeros(1, 3, 2, 64, requires_grad=True)
+    k = torch.zeros(1, 3, 1, 64, requires_grad=True)
+    lead = torch.zeros(shift)
+    qo, ko = G.qk_norm_rope(q, k, None)
+    flat = torch.cat([lead, qo.flatten(), ko.flatten()])
+    held = {}
+    bwd = _attn.qk_norm_rope_bwd
+
+    def spy(q, k, dq, dk, *a, **kw):
+        held.update(dq=dq, dk=dk)
+        return bwd(q, k, dq, dk, *a, **kw)
+
+    monkeypatch.setattr(_attn, "qk_norm_rope_bwd", spy)
+    grad = torch.arange(flat.numel(), dtype=torch.float32)
+    flat.backward(grad)
+    (name, args), = [x for x in seen if x[0].endswith("bwd")]
+    assert [args[2], args[3]] == [held["dq"].data_ptr(), held["dk"].data_ptr()]
+    for t, at in ((held["dq"], shift), (held["dk"], shift + qo.numel())):
+        assert t.is_contiguous() and t.data_ptr() % 16 == 0
+        assert torch.equal(t.flatten(), grad[at:at + t.numel()])
+
+
+@pytest.mark.parametrize("shift", [0, 3])
+def test_mixer_gradients_at_any_offset(monkeypatch, shift):
+    """The same for the mixer's gradients of outputs and final states."""
+    import gated_delta_rule_36_amd as G
+    held = {}
+    x = torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16, requires_grad=True)
+    s0 = torch.zeros(1, 2, 64, 64)
+    monkeypatch.setattr(_lib, "chunk_fwd_train",
+                        lambda q, *a, **kw: (torch.zeros_like(q), torch.zeros_like(s0), None))
+
+    def spy(q, k, v, g, b, w, do, d_final_state=None, **kw):
+        held.update(do=do, ds=d_final_state)
+        return (torch.zeros_like(q),) * 6 + (torch.zeros_like(s0),)
+
+    monkeypatch.setattr(_lib, "chunk_bwd", spy)
+    o, s = G.gated_delta_rule2(x, x, x, x, x, x)
+    flat = torch.cat([torch.zeros(shift, dtype=torch.bfloat16), o.flatten()])
+    states = torch.cat([torch.zeros(shift), s.flatten()])
+    grads = [(torch.arange(t.numel()) % 251).to(t.dtype) for t in (flat, states)]
+    torch.autograd.backward((flat, states), grads)
+    for t, g in ((held["do"], grads[0]), (held["ds"], grads[1])):
+        assert t.is_contiguous() and t.data_ptr() % 16 == 0 and torch.equal(t.flatten(), g[shift:])
+
+
 def test_serving_binding_refusals(anywhere):
     import gated_delta_rule_36_amd as G
     cache = G.kv_cache(6, 2, 64, device="cpu")
