@@ -162,7 +162,8 @@ def qk_norm_rope_fwd(q, k, inv_freq, positions=None, q_weight=None, k_weight=Non
     positions: int32 [B, T] or None (0 .. T - 1 in every sequence). interleaved: pairs
     (2i, 2i + 1) instead of (i, i + rot / 2). norm=False leaves the mean square out. q and k may
     be slices of one projection (a token's rows dense, tokens at one stride). out: optional
-    contiguous pair, written and returned (q and k themselves where they are contiguous).
+    contiguous pair, written and returned (q and k themselves where they are contiguous); not
+    tensors that require gradients, unless under no_grad.
     Returns (q_out, k_out)."""
     B, T, Hq, Hk, d, qs, ks, rot, code, dev, dt = _norm_rope_args(q, k, inv_freq, positions,
                                                                   q_weight, k_weight)
@@ -172,6 +173,9 @@ def qk_norm_rope_fwd(q, k, inv_freq, positions=None, q_weight=None, k_weight=Non
         qo, ko = out
         _dense("out[0]", qo, (B, T, Hq, d), dt, dev)
         _dense("out[1]", ko, (B, T, Hk, d), dt, dev)
+        if (qo.requires_grad or ko.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("out: the tensors require gradients, which would not know of this "
+                             "call; use qk_norm_rope, or no_grad")
     _call("gdn2_qk_norm_rope", dev, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
           _p(positions), _p(inv_freq), qo.data_ptr(), ko.data_ptr(), B, T, Hq, Hk, d, qs, ks, rot,
           eps, _flags(interleaved, norm), code)

@@ -219,6 +219,20 @@ def test_norm_rope_binding_refusals(anywhere):
         G.qk_norm_rope_bwd(q, k, q, k.float(), fr)
 
 
+def test_norm_rope_in_place_under_autograd_is_refused(anywhere):
+    """Written in place, tensors with a history would keep the gradients of the unrotated rows."""
+    import gated_delta_rule_36_amd as G
+    leaf = torch.zeros(1, 2, 2, 64, requires_grad=True)
+    q, k = leaf * 1, torch.zeros(1, 2, 2, 64)
+    for out in ((q, k), (k, q)):
+        with pytest.raises(ValueError, match="gradients"):
+            G.qk_norm_rope_fwd(q, k, None, out=out)
+        with torch.no_grad(), pytest.raises(anywhere):
+            G.qk_norm_rope_fwd(q, k, None, out=out)
+    with pytest.raises(anywhere):
+        G.qk_norm_rope_fwd(q, k, None, out=(torch.empty_like(k), k))
+
+
 @pytest.mark.parametrize("shift", [0, 3, 5])
 def test_gradients_at_any_offset(monkeypatch, shift):
     """Autograd's gradients may be views that start anywhere (here behind `shift` elements of one flat
