@@ -210,6 +210,36 @@ def test_autograd_equals_the_calls():
     assert torch.equal(leaf.grad, one)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_autograd_through_one_projection(dt):
+    """Queries and keys as slices of a projection that is the leaf, with the values between them and
+    the gradient, which comes back as views of one flat tensor."""
+    import gated_delta_rule_36_amd as G
+    B, T, Hq, Hk, d, rot = 2, 21, 4, 2, 64, 64
+    rng = np.random.default_rng(17)
+    x = draw(rng, B, T, (Hq + 2 * Hk) * d + 8, dtype=DT[dt]).cuda().requires_grad_()
+    w = [torch.from_numpy((1 + 0.2 * rng.standard_normal(d)).astype(np.float32)).cuda().requires_grad_() for _ in range(2)]
+    fr = inv_freq(rot)
+    say("qk_norm_rope autograd through a projection", dt)
+    q = x[..., : Hq * d].view(B, T, Hq, d)
+    k = x[..., Hq * d: (Hq + Hk) * d].view(B, T, Hk, d)
+    v = x[..., (Hq + Hk) * d: (Hq + 2 * Hk) * d]
+    y = G.qk_norm_rope(q, k, torch.from_numpy(fr).cuda(), q_weight=w[0], k_weight=w[1])
+    lead = torch.zeros(3, dtype=DT[dt], device="cuda")
+    flat = torch.cat([lead, y[0].flatten(), y[1].flatten(), v.flatten()])
+    grad = draw(rng, flat.numel(), dtype=DT[dt]).cuda()
+    flat.backward(grad)
+    torch.cuda.synchronize()
+    gq, gk, gv = (f64(g) for g in grad[3:].split([B * T * h * d for h in (Hq, Hk, Hk)]))
+    got = f64(x.grad)
+    pos = np.tile(np.arange(T), (B, 1))
+    for i, (name, t, g, H, at) in enumerate((("q", q, gq, Hq, 0), ("k", k, gk, Hk, Hq * d))):
+        dx, dw, bx, bw = _bwd_bound(f64(t), g.reshape(B, T, H, d), f64(w[i]), pos, fr, DT[dt], 1e-6, False, True)
+        assert_within("d" + name, got[..., at: at + H * d].reshape(dx.shape), dx, bx)
+        assert_within(f"d{name}_weight", w[i].grad, dw, bw)
+    assert np.array_equal(got[..., (Hq + Hk) * d: -8].ravel(), gv) and not got[..., -8:].any()
+
+
 def test_second_derivatives_are_refused():
     import gated_delta_rule_36_amd as G
     q, k, pos, w, rng = _case(15, 1, 3, 2, 2, 64, 64, "fp32")
