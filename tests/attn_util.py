@@ -124,3 +124,41 @@ def attention_ref(q, paged, lens, spans, window=0, scale=None, few=False):
         o[first:first + count] = o_i
         bound[first:first + count] = (e + w + 64 * U + U * max(total, 1) ** 0.5) * spread + hb * np.abs(o_i) + 1e-38
     return o, bound
+
+
+def half_step(x, dtype):
+    """Half the distance of dtype's values around |x|."""
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(x), torch.finfo(dtype).tiny)))) * torch.finfo(dtype).eps
+    return step / 2
+
+
+def few_rows_ref(q, paged, lens, L, window=0, round_weights=None):
+    """Rows q [N, L, Hq, d] (float64) over blocks that all exist, and a bound near the output's own
+    rounding, for kernels whose weights keep more bits than the output's type. As in attention_ref
+    the weights are off by at most e = 2 (d U A + 4 U + 2 U A) and the sums by 64 U + U sqrt(keys),
+    and the square of bf16's half step for a weight as two terms, but A is the largest sum|q k| scale
+    of a key that the row sees, and the output's rounding the half step around its own value. round_weights: applied to the weights (relative to the row's
+    largest) of the product, their sum staying as it is."""
+    N, _, Hq, d = q.shape
+    G = Hq // paged.Hk
+    o, bound = np.zeros(q.shape), np.zeros(q.shape)
+    for n in range(N):
+        total = int(lens[n])
+        slots = paged.table[n, : -(-total // B64)]
+        for i in range(L):
+            p = total - L + i
+            low = max(0, p + 1 - window) if window else 0
+            if p < 0:
+                continue
+            for h in range(Hq):
+                k, v = ((x[slots, h // G] * s[slots, h // G][:, None, None]).reshape(-1, d)[low:p + 1] for x, s in
+                        ((paged.ref.k, paged.ref.k_scale), (paged.ref.v, paged.ref.v_scale)))
+                x = k @ q[n, i, h] * d ** -0.5
+                w = np.exp(x - x.max())
+                wr = w if round_weights is None else round_weights(w)
+                o[n, i, h] = wr @ v / w.sum()
+                A = (np.abs(k) @ np.abs(q[n, i, h])).max() * d ** -0.5
+                e = 2 * (d * U * A + 4 * U + 2 * U * A) + half(torch.bfloat16) ** 2 + 64 * U + U * total ** 0.5
+                b = e * (w @ np.abs(v)) / w.sum()
+                bound[n, i, h] = b + half_step(np.abs(o[n, i, h]) + b, torch.bfloat16) + 1e-38
+    return o, bound

@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from oracle import gdn2_attn as R
-from tests.attn_util import (B64, U, Paged, assert_within, attention_ref, draw, f64, half, inv_freq,
-                             rows_bound)
+from tests.attn_util import (B64, U, Paged, assert_within, attention_ref, draw, f64, few_rows_ref, half,
+                             inv_freq, rows_bound)
 from tests.gpu_util import say
 
 pytestmark = pytest.mark.gpu
@@ -294,6 +294,25 @@ def test_attention_few_rows(G, L, d, window):
     paged.fill(rng)
     say("cache_attention few rows", G, L, d, window)
     _attention(rng, paged, [L] * len(lens), lens, 2 * G, window=window, alias=L == 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,L,longest,window", [(4, 1, 449, 0), (4, 1, 449, 70), (3, 5, 1000, 0), (8, 4, 1000, 70),
+                                                (16, 1, 1000, 0), (2, 2, 6001, 0)])
+def test_attention_few_rows_at_the_outputs_rounding(G, L, longest, window, d):
+    """Single tokens and drafts are off by the output's own rounding and little more: weights rounded
+    once to bf16 would be 4 to 35 times the bound somewhere."""
+    import gated_delta_rule_36_amd as G_
+    rng = np.random.default_rng(G * 7 + L + d + window)
+    lens = [L, 64, 65, 127 + L, longest]
+    paged = Paged(rng, lens, 2, d)
+    paged.fill(rng, spread=0.3)
+    say("cache_attention few rows at the output's rounding", G, L, longest, window, d)
+    q = draw(rng, len(lens), L, 2 * G, d)
+    got = G_.cache_attention(q.cuda(), paged.dev, paged.table_t(), _i32(lens), window=window)
+    torch.cuda.synchronize()
+    ref, bound = few_rows_ref(f64(q), paged, lens, L, window)
+    assert_within("o", got, ref, bound)
 
 
 @pytest.mark.parametrize("d", [64, 128])

@@ -5,8 +5,10 @@ import itertools
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import gdn2_attn as R
+from tests.attn_util import Paged, draw, f64, few_rows_ref
 
 
 def _rows(seed, T=3, H=2, d=16):
@@ -161,3 +163,23 @@ def test_attention_over_missing_blocks_is_that_over_the_rest():
             w = np.exp(kk @ q[i, h] * 8 ** -0.5)
             assert np.allclose(o[i, h], w @ vv / w.sum(), atol=1e-12)
     assert np.isfinite(spread).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,L,window", [(4, 1, 0), (3, 5, 70), (8, 4, 0)])
+def test_few_rows_bound_tells_one_rounding_of_the_weights_from_two_terms(G, L, window, d):
+    """The bound that the few-row kernel is held to takes weights as two bf16 terms and rejects
+    weights rounded once."""
+    rng = np.random.default_rng(G * 7 + L + d + window)
+    lens = [L, 64, 65, 127 + L, 449]
+    paged = Paged(rng, lens, 2, d, device="cpu")
+    paged.fill(rng, spread=0.3)
+    q = f64(draw(rng, len(lens), L, 2 * G, d))
+    bf = lambda x: torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+    ref, bound = few_rows_ref(q, paged, lens, L, window)
+    for n, total in enumerate(lens):
+        assert np.allclose(R.attention(q[n], paged.ref, paged.table[n], total, window)[0], ref[n], atol=1e-12)
+    two, _ = few_rows_ref(q, paged, lens, L, window, lambda w: bf(w) + bf(w - bf(w)))
+    assert (np.abs(bf(two) - ref) <= bound).all()
+    one, _ = few_rows_ref(q, paged, lens, L, window, bf)
+    assert (np.abs(bf(one) - ref) > 3 * bound).any()
