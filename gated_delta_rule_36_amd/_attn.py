@@ -284,8 +284,10 @@ def attn_prologue(q, k, v, cache, block_table, seq_lens, inv_freq, cu_seqlens=No
     [1, T, H, d] with cu_seqlens int32 [N + 1]; cache: a KVCache; block_table: int32
     [N, max_blocks], entries outside [0, P) naming no block; seq_lens: int32 [N], all tokens of
     each sequence with the new ones, which are its last. A sequence with fewer tokens than new
-    rows has its leading rows as padding (zeros in the result). A block that is written must stand
-    in the table once. out: optional contiguous result, which may be q.
+    rows has its leading rows as padding (zeros in the result); rows behind the last packed
+    sequence are not written (undefined where out is None). A block that is written must stand in
+    the table once. q, k and v are what the projections give: their norm and rotation happen here.
+    out: optional contiguous result, which may be q.
     Returns q_out, [.., Hq, d]."""
     B, T, Hq, Hk, d, N, P, MB, dev = _cache_args(q, cache, block_table, seq_lens, cu_seqlens)
     qs = _token_stride("q", q, q.shape)
@@ -322,7 +324,9 @@ def cache_attention(q, cache, block_table, seq_lens, cu_seqlens=None, window=0, 
     q: [N, T, Hq, d] bf16 contiguous, or packed [1, T, Hq, d] with cu_seqlens int32 [N + 1];
     cache, block_table, seq_lens: as for attn_prologue. Query i of a sequence of length S with T
     new rows stands at p = S - T + i and sees the keys j <= p, with window > 0 only those with
-    j > p - window. scale: 1 / sqrt(d) where None. Rows that see no key come out zero. out:
+    j > p - window. scale: 1 / sqrt(d) where None. Rows that see no key come out zero; rows behind
+    the last packed sequence are not written (undefined where out is None). The work is cut by the
+    block table's width: a table much wider than the sequences need makes small calls slower. out:
     optional contiguous result (may be q). workspace: optional uint8 device tensor of at least
     cache_attention_workspace_bytes(...), allocated when None; calls that can overlap, captured
     ones among them, need one each.

@@ -455,7 +455,9 @@ enum { GDN2_CACHE_BLOCK = 64 };
  *   not count for the scales: every query of that head which attends to it comes out NaN, others
  *   are not touched.
  *   q, k, v : rows as in gdn2_qk_norm_rope, strides of their own
- *   q_out   : dense [.., Hq, d]; zeros in rows without a token; may be q where that is dense
+ *   q_out   : dense [.., Hq, d]; zeros in rows without a token (padding); rows in front of the
+ *             first packed sequence and behind the last are not written; may be q where that is
+ *             dense
  *   A block that this call writes must stand in the table once.
  *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk. No tokens: a no-op.
  * Returns GDN2_OK or an error status.
@@ -472,14 +474,22 @@ int gdn2_attn_prologue(const void* q, const void* k, const void* v, const float*
  * Causal attention of the new rows over the cache, which already holds their own keys and
  * values:  o_i = sum_j softmax_j(scale q_i . k_j) v_j,  j <= p_i, and j > p_i - window where
  * window > 0. Query head h reads kv head h / (Hq / Hk). A row that sees no key (padding, an
- * empty sequence, blocks that do not exist) is written as zeros; rows behind the last packed
- * sequence are not written.
+ * empty sequence, blocks that do not exist) is written as zeros; rows in front of the first packed
+ * sequence and behind the last are not written.
+ * Up to 32 rows (tokens of the call per sequence, or in all when packed, times Hq / Hk) the weights
+ * enter the second product as two bf16 terms, and the result is off by its own rounding; above, as
+ * in prompts, they are rounded once to bf16 (2.2e-3 relative in the 2-norm against 64 bits, where
+ * the result's rounding alone is 1.7e-3). Sequences of few rows in a packed call may go either way.
  *   q, o      : dense [B, T, Hq, d] (dtype); o may be q
  *   scale     : positive and finite, usually 1 / sqrt(d)
  *   workspace : at least gdn2_cache_attention_workspace_bytes(...) bytes (0: may be NULL),
  *               16-byte aligned, free for the call's duration on `hip_stream`. A captured call
  *               uses it at every replay: two graphs that may run at once need one each.
- *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk. No tokens: a no-op.
+ *   max_blocks : the key axis is cut for sequences that fill the table, as their lengths are on the
+ *               device. A table several times as wide as they need makes calls of few rows or few
+ *               tiles two to three times slower: pass no more columns than the longest may need.
+ *   Supported: GDN2_BF16, d in {64, 128}, Hq a multiple of Hk, B * T * Hq below 2^31 - 1024. No
+ *   tokens: a no-op.
  * Returns GDN2_OK or an error status.
  */
 int gdn2_cache_attention(const void* q, const void* k_cache, const void* v_cache,
