@@ -16,8 +16,8 @@
 //    or two 16-column tiles; bound by reading the cache. Each wave owns whole blocks, straight
 //    from global memory to registers, with no barrier until the waves merge; the key axis is
 //    cut over workgroups.
-//  * many rows (prompts): 128 query rows a workgroup, 32 a wave, blocks converted once to bf16
-//    in LDS (double buffered); bound by the matrix cores and exp2.
+//  * many rows (prompts): 128 or 256 query rows a workgroup, 32 a wave, blocks converted once to
+//    bf16 in LDS (double buffered); bound by the matrix cores and exp2.
 // Where the key axis is cut, each piece leaves (maximum, sum, output) in the workspace and a
 // merge kernel joins them in a fixed order.
 
@@ -613,8 +613,8 @@ gdn2_cache_attn_tile_kernel(CacheAttnArgs A, int units, int split_blocks, Pieces
     const float inv = l == 0.f ? 0.f : 1.f / l;
     // The rows pass through the wave's own part of LDS (nobody reads tiles there any more) and
     // leave in whole lines, past the caches, so that they are out before the kernel's end has to
-    // write the caches back (8192 tokens, window 512, 8 heads: 74 us as they lie, in pieces of 16
-    // bytes; 69 in lines; 66 in lines past the caches).
+    // write the caches back (8192 tokens, window 514, 16 heads on 8, when it was changed: 74 us as
+    // they lie, in pieces of 16 bytes; 69 in lines; 66 in lines past the caches; now 55 to 61).
     constexpr int LR = D / 8, RP = 64 / LR;  // lanes of a row, rows of a pass
     bf16* const own = reinterpret_cast<bf16*>(&lds) + wave * 32 * KLD;
 #pragma unroll
@@ -811,7 +811,9 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
   };
   const long nb = reach(T);
   // The few-row kernel's pieces. The lengths are on the device, so the cut goes by the table's
-  // width; pieces past a sequence's end leave at once.
+  // width: pieces past a sequence's end leave at once, and the others are as long as for a sequence
+  // that fills the table (8 sequences of 4096 tokens, 8 kv heads: 16.7 us with a table of 64 blocks,
+  // 21.7 of 128, 33.7 of 512).
   const auto cut = [&](long nb, int row_tiles, int& waves, int& split_blocks, int& splits) {
     const long groups = (long)N * Hk;
     // A workgroup a compute unit: twice or half as many pieces cost 15 to 25% (4 sequences of 32 K
@@ -868,8 +870,9 @@ CacheAttnPlan cache_attn_plan(bool packed, int N, int T, int Hq, int Hk, int d, 
     }
     const long per = best == 1 ? nb : (most + best - 1) / best;
     // Eight waves on one staged copy of K and V where there are tiles enough: 255 against 280 us
-    // (8192 tokens); but 57 against 47 us where a tile has only 9 blocks (1024 tokens, window 512),
-    // and 181 against 170 us at d = 64 (8192 tokens), where a block has half as much to stage.
+    // (8192 tokens, 16 heads on 4); but 48 against 45 us where a tile has only 9 blocks (8 x 1024
+    // tokens, window 512; 23 against 16 of one sequence), and at d = 64 a block has only half as
+    // much to stage as 512 threads take at once.
     p.tile_rows = best == 1 && d == 128 && most > 24 && tiles(256) * Hk >= 512 ? 256 : 128;
     p.row_tiles = (int)(packed ? tiles(p.tile_rows) : tiles(p.tile_rows) / N);
     p.split_blocks = (int)per;
