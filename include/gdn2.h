@@ -480,6 +480,8 @@ int gdn2_attn_prologue(const void* q, const void* k, const void* v, const float*
  * enter the second product as two bf16 terms, and the result is off by its own rounding; above, as
  * in prompts, they are rounded once to bf16 (2.2e-3 relative in the 2-norm against 64 bits, where
  * the result's rounding alone is 1.7e-3). Sequences of few rows in a packed call may go either way.
+ * The output is divided by the sum of its weights at the end, so the sum of |v| over the keys that a
+ * row sees has to stay below 2^120.
  *   q, o      : dense [B, T, Hq, d] (dtype); o may be q
  *   scale     : positive and finite, usually 1 / sqrt(d)
  *   workspace : at least gdn2_cache_attention_workspace_bytes(...) bytes (0: may be NULL),
