@@ -94,6 +94,24 @@ def lib():
         L.gdn2_cache_attention.restype = _I
         L.gdn2_cache_attention_workspace_bytes.argtypes = [_I] * 9
         L.gdn2_cache_attention_workspace_bytes.restype = _Z
+        L.gdn2_linear_recurrence.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P]
+        L.gdn2_linear_recurrence.restype = _I
+        L.gdn2_linear_recurrence_states_bytes.argtypes = [_I] * 5
+        L.gdn2_linear_recurrence_states_bytes.restype = _Z
+        L.gdn2_linear_recurrence_bwd.argtypes = [_P] * 11 + [_I] * 4 + [_I64] * 3 + [_I, _P]
+        L.gdn2_linear_recurrence_bwd.restype = _I
+        L.gdn2_linear_recurrence_tokens.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P]
+        L.gdn2_linear_recurrence_tokens.restype = _I
+        L.gdn2_residual_norm.argtypes = ([_P] * 6 + [_I64, _I, _I64, _I64, _I, _F, _I, _I, _P])
+        L.gdn2_residual_norm.restype = _I
+        L.gdn2_residual_norm_bwd.argtypes = [_P] * 7 + [_I64, _I, _I64, _F, _I, _I, _P, _Z, _P]
+        L.gdn2_residual_norm_bwd.restype = _I
+        L.gdn2_residual_norm_bwd_workspace_bytes.argtypes = [_I64, _I]
+        L.gdn2_residual_norm_bwd_workspace_bytes.restype = _Z
+        L.gdn2_verify_drafts.argtypes = [_P] * 7 + [_I] * 4 + [_P, _Z, _P]
+        L.gdn2_verify_drafts.restype = _I
+        L.gdn2_verify_drafts_workspace_bytes.argtypes = [_I] * 2
+        L.gdn2_verify_drafts_workspace_bytes.restype = _Z
         L.gdn2_status_string.argtypes = [_I]
         L.gdn2_status_string.restype = ctypes.c_char_p
         L.gdn2_version.argtypes = []

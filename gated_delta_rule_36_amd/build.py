@@ -18,7 +18,8 @@ BUILD_INFO = os.path.join(PKG, "build_info.json")
 
 SOURCES = ["gdn2_api.cpp", "gdn2_chunk.hip", "gdn2_split.hip", "gdn2_bwd.hip", "gdn2_decode.hip",
            "gdn2_block.hip", "gdn2_noalloc.hip", "gdn2_attn_api.cpp", "gdn2_attn_rows.hip",
-           "gdn2_attn.hip",
+           "gdn2_attn.hip", "gdn2_stack_api.cpp", "gdn2_recurrence.hip", "gdn2_norm.hip",
+           "gdn2_verify.hip",
            "gdn2_fwd.hip", "gdn2_recurrent.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

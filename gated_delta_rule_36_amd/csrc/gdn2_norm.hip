@@ -1,0 +1,369 @@
+// The norm between the layers of a stack on gfx950, with the residual's addition:
+//     h = x + r          (stored in r's type: the stream that the next layer adds to)
+//     y = h rho weight,  rho = 1 / sqrt(mean(h^2) + eps)   (of h as it is stored)
+// y in x's type, or in 8 bits for the next projection: e4m3 codes with one power-of-two scale for
+// every group of channels, the smallest s >= 2^-64 with max|y| <= 448 s. And the gradients, with
+// u = dy weight and n = h rho:
+//     dh_total = dh + rho (u - n mean(u n)) = dx = dr,   dweight = sum over rows of dy n.
+//
+// Bound by HBM: every row is read once and kept in registers between the sum and the output. A row
+// belongs to one wave (no barrier) or, where rows are few or wide, to the 4 waves of a workgroup.
+
+#include <type_traits>
+
+#include "gdn2_attn_device.h"
+#include "gdn2_stack_launch.h"
+
+namespace gdn2 {
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ T wave_sum(T x) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
+  return x;
+}
+
+// Sum over the W waves of a row: W = 4 through LDS (s: 4 values of this call's own).
+template <int W, typename T>
+__device__ __forceinline__ T row_total(T x, T* s, int wave) {
+  x = wave_sum(x);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) s[wave] = x;
+    __syncthreads();
+    x = ((s[0] + s[1]) + (s[2] + s[3]));
+    __syncthreads();
+  }
+  return x;
+}
+
+// 2^k with the smallest k in [-64, 126] for which amax <= 448 * 2^k; NaN and zero give 2^-64.
+__device__ __forceinline__ float power_scale(double amax) {
+  if (!(amax > 0)) return __uint_as_float((127 - 64) << 23);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, amax);
+  int e = (int)(bits >> 52) - 1022;  // amax = m 2^e, m in [0.5, 1) (doubles: never subnormal here)
+  const bool high = (bits & ((1ull << 52) - 1)) > 0xC000000000000ull;  // m > 0.875
+  e = e - (high ? 8 : 9);
+  e = e < -64 ? -64 : e > 126 ? 126 : e;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ double lanes_max(double x, int lanes) {
+  for (int m = 1; m < lanes; m <<= 1) {
+    const double y = __shfl_xor(x, m, 64);
+    x = x > y || x != x ? x : y;  // a NaN stays
+  }
+  return x;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(const float* f) {
+  const int r = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], r, true);
+}
+
+}  // namespace
+
+// E steps of 8 channels a lane; W waves a row. BITS8: the output in 8 bits. There the mean square
+// and the groups' maxima are formed in fp64 (h and weight are exact in it, so is their product):
+// the scale steps where a maximum passes 448 times a power of two, and must not step by a rounding.
+template <typename T, typename TR, int E, int W, bool ADD, bool BITS8>
+__global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArgs a) {
+  typedef typename std::conditional<BITS8, double, float>::type acc;
+  __shared__ acc s_sum[4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long row = W == 1 ? (long)blockIdx.x * 4 + wave : (long)blockIdx.x;
+  if (W == 1 && row >= a.rows) return;
+  const int part = W == 1 ? 0 : wave;
+  const T* x = (const T*)a.x + row * a.x_stride;
+  const TR* r = ADD ? (const TR*)a.r + row * a.r_stride : nullptr;
+  Vec8<T> rx[E];
+  Vec8<TR> rr[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int ch = ((e * W + part) * 64 + lane) * 8;
+    if (ch < a.D) {
+      rx[e].load(x + ch);
+      if constexpr (ADD) rr[e].load(r + ch);
+    }
+  }
+  float h[E][8];
+  acc ss = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int ch = ((e * W + part) * 64 + lane) * 8;
+    if (ch < a.D) {
+      rx[e].to_float(h[e]);
+      if constexpr (ADD) {
+        float f[8];
+        rr[e].to_float(f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) h[e][c] = to_f(from_f<TR>(h[e][c] + f[c]));
+        store8((TR*)a.h + row * a.D + ch, h[e]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) h[e][c] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) ss += (acc)h[e][c] * (acc)h[e][c];
+  }
+  ss = row_total<W>(ss, s_sum, wave);
+  if constexpr (!BITS8) {
+    const float rho = rsqrtf(ss / a.D + a.eps);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      if (ch < a.D) {
+        const f4 w0 = reinterpret_cast<const f4*>(a.weight + ch)[0], w1 = reinterpret_cast<const f4*>(a.weight + ch)[1];
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] = h[e][c] * rho * (c < 4 ? w0[c] : w1[c - 4]);
+        store8((T*)a.y + row * a.D + ch, y);
+      }
+    }
+  } else {
+    const double rho = 1.0 / sqrt(ss / a.D + (double)a.eps);
+    const float rho32 = (float)rho;
+    const bool whole = a.group >= a.D;  // one scale a row (128 channels or fewer: the row itself)
+    const int lanes = whole ? 64 : a.group / 8;
+    double big[E], most = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      big[e] = 0;
+      if (ch < a.D) {
+        const f4 w0 = reinterpret_cast<const f4*>(a.weight + ch)[0], w1 = reinterpret_cast<const f4*>(a.weight + ch)[1];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float w = c < 4 ? w0[c] : w1[c - 4];
+          const double p = fabs((double)h[e][c] * (double)w);
+          big[e] = big[e] > p || big[e] != big[e] ? big[e] : p;
+          h[e][c] = h[e][c] * rho32 * w;
+        }
+      }
+      most = most > big[e] || most != most ? most : big[e];
+    }
+    if (whole) {
+      most = lanes_max(most, 64);
+      if constexpr (W > 1) {
+        if (lane == 0) s_sum[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const double y = s_sum[u];
+          most = most > y || most != most ? most : y;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const float s = power_scale((whole ? most : lanes_max(big[e], lanes)) * rho);
+      if (ch < a.D) {
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));  // 1 / s, exact
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] = h[e][c] * inv;
+        *reinterpret_cast<uint2*>((uint8_t*)a.y + row * a.D + ch) = make_uint2(e4m3x4(f), e4m3x4(f + 4));
+        if (ch % a.group == 0) a.scale[row * (a.D / a.group) + ch / a.group] = s;
+      }
+    }
+  }
+}
+
+// Gradients. A wave (or workgroup) walks rows and keeps its part of the weight's gradient in
+// registers; each workgroup leaves one partial sum, which the second kernel adds in a fixed order.
+template <typename T, typename TR, int E, int W, bool DH>
+__global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
+  __shared__ __attribute__((aligned(16))) float s_part[W == 1 ? 4 : 1][W == 1 ? E * 512 : 8];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = W == 1 ? 0 : wave;
+  float w[E][8], dw[E][8];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int ch = ((e * W + part) * 64 + lane) * 8;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) w[e][c] = dw[e][c] = 0.f;
+    if (ch < a.D) {
+      const f4 w0 = reinterpret_cast<const f4*>(a.weight + ch)[0], w1 = reinterpret_cast<const f4*>(a.weight + ch)[1];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[e][c] = c < 4 ? w0[c] : w1[c - 4];
+    }
+  }
+  const long step = (long)gridDim.x * (W == 1 ? 4 : 1);
+  for (long row = W == 1 ? (long)blockIdx.x * 4 + wave : (long)blockIdx.x; row < a.rows; row += step) {
+    Vec8<T> rg[E];
+    Vec8<TR> rh[E], rd[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      if (ch < a.D) {
+        rg[e].load((const T*)a.dy + row * a.D + ch);
+        rh[e].load((const TR*)a.h + row * a.h_stride + ch);
+        if constexpr (DH) rd[e].load((const TR*)a.dh + row * a.D + ch);
+      } else {
+        rg[e].zero();
+        rh[e].zero();
+      }
+    }
+    float ss = 0.f, uh = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float g[8], h[8];
+      rg[e].to_float(g);
+      rh[e].to_float(h);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        ss = fmaf(h[c], h[c], ss);
+        uh = fmaf(g[c] * w[e][c], h[c], uh);
+      }
+    }
+    if constexpr (W == 1) {
+      ss = wave_sum(ss);
+      uh = wave_sum(uh);
+    } else {
+      ss = wave_sum(ss);
+      uh = wave_sum(uh);
+      if (lane == 0) {
+        s_part[0][wave] = ss;
+        s_part[0][4 + wave] = uh;
+      }
+      __syncthreads();
+      ss = (s_part[0][0] + s_part[0][1]) + (s_part[0][2] + s_part[0][3]);
+      uh = (s_part[0][4] + s_part[0][5]) + (s_part[0][6] + s_part[0][7]);
+      __syncthreads();
+    }
+    const float rho = rsqrtf(ss / a.D + a.eps);
+    const float back = rho * rho * (uh / a.D);  // rho mean(u n)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      if (ch < a.D) {
+        float g[8], h[8], d[8];
+        rg[e].to_float(g);
+        rh[e].to_float(h);
+        if constexpr (DH) rd[e].to_float(d);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float t = rho * (g[c] * w[e][c] - h[c] * back);
+          dw[e][c] = fmaf(g[c], h[c] * rho, dw[e][c]);
+          d[c] = DH ? d[c] + t : t;
+        }
+        store8((T*)a.dx + row * a.D + ch, d);
+        if constexpr (sizeof(T) != sizeof(TR)) store8((TR*)a.dr + row * a.D + ch, d);
+      }
+    }
+  }
+  float* const out = a.partial + (long)blockIdx.x * a.D;
+  if constexpr (W == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store8(&s_part[wave][(e * 64 + lane) * 8], dw[e]);
+    __syncthreads();
+    for (int ch = threadIdx.x * 4; ch < a.D; ch += 1024) {
+      f4 s = *reinterpret_cast<const f4*>(&s_part[0][ch]);
+#pragma unroll
+      for (int u = 1; u < 4; ++u) s += *reinterpret_cast<const f4*>(&s_part[u][ch]);
+      *reinterpret_cast<f4*>(out + ch) = s;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = ((e * W + part) * 64 + lane) * 8;
+      if (ch < a.D) store8(out + ch, dw[e]);
+    }
+  }
+}
+
+// The weight's gradient: 8 channels a workgroup, 32 lanes each walking the partial sums.
+__global__ void __launch_bounds__(256) gdn2_residual_norm_dweight_kernel(const float* partial, float* dweight, int D, int groups) {
+  __shared__ float s[32][8];
+  const int c = threadIdx.x & 7, k = threadIdx.x >> 3;
+  float x = 0.f;
+  for (int g = k; g < groups; g += 32) x += partial[(long)g * D + blockIdx.x * 8 + c];
+  s[k][c] = x;
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    dweight[blockIdx.x * 8 + threadIdx.x] = t;
+  }
+}
+
+namespace {
+
+// Waves of a row: one up to 2048 channels, unless rows are too few to fill the card.
+int waves_of(long rows, int D) { return D > 2048 || rows < 1024 ? 4 : 1; }
+
+// Calls f(E) with the steps of a lane for D channels and W waves.
+template <typename F>
+hipError_t with_steps(int D, int W, F f) {
+  const int e = (D + W * 512 - 1) / (W * 512);
+  if (e <= 1) return f(std::integral_constant<int, 1>());
+  if (e <= 2) return f(std::integral_constant<int, 2>());
+  if (e <= 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 8>());
+}
+
+template <typename T, typename TR, int W>
+hipError_t norm_launch(const ResidualNormArgs& a) {
+  return with_steps(a.D, W, [&](auto steps) {
+    constexpr int E = decltype(steps)::value;
+    const dim3 grid((unsigned)(W == 1 ? (a.rows + 3) / 4 : a.rows)), block(256);
+    const hipStream_t st = (hipStream_t)a.stream;
+    if constexpr (W == 4 || E <= 4) {
+      if (a.scale) {
+        if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, true, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, false, true>), grid, block, 0, st, a);
+      } else {
+        if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, true, false>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, false, false>), grid, block, 0, st, a);
+      }
+    }
+    return hipGetLastError();
+  });
+}
+
+template <typename T, typename TR, int W>
+hipError_t norm_bwd_launch(const ResidualNormBwdArgs& a) {
+  const int groups = residual_norm_bwd_groups(a.rows, a.D);
+  const hipStream_t st = (hipStream_t)a.stream;
+  const hipError_t err = with_steps(a.D, W, [&](auto steps) {
+    constexpr int E = decltype(steps)::value;
+    const dim3 grid((unsigned)groups), block(256);
+    if constexpr (W == 4 || E <= 4) {
+      if (a.dh) hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, E, W, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, E, W, false>), grid, block, 0, st, a);
+    }
+    return hipGetLastError();
+  });
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(gdn2_residual_norm_dweight_kernel, dim3((unsigned)(a.D / 8)), dim3(256), 0, st, a.partial, a.dweight, a.D, groups);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int residual_norm_bwd_groups(long rows, int D) {
+  const long full = waves_of(rows, D) == 1 ? (rows + 3) / 4 : rows;
+  return (int)(full < 512 ? full : 512);
+}
+
+hipError_t launch_residual_norm(const ResidualNormArgs& a) {
+  const bool one = waves_of(a.rows, a.D) == 1;
+  if (a.dtype == 1) return one ? norm_launch<float, float, 1>(a) : norm_launch<float, float, 4>(a);
+  if (a.r_dtype == 1) return one ? norm_launch<bf16, float, 1>(a) : norm_launch<bf16, float, 4>(a);
+  return one ? norm_launch<bf16, bf16, 1>(a) : norm_launch<bf16, bf16, 4>(a);
+}
+
+hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a) {
+  const bool one = waves_of(a.rows, a.D) == 1;
+  if (a.dtype == 1) return one ? norm_bwd_launch<float, float, 1>(a) : norm_bwd_launch<float, float, 4>(a);
+  if (a.r_dtype == 1) return one ? norm_bwd_launch<bf16, float, 1>(a) : norm_bwd_launch<bf16, float, 4>(a);
+  return one ? norm_bwd_launch<bf16, bf16, 1>(a) : norm_bwd_launch<bf16, bf16, 4>(a);
+}
+
+}  // namespace gdn2

@@ -504,6 +504,130 @@ int gdn2_cache_attention(const void* q, const void* k_cache, const void* v_cache
 size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, int Hk, int d, int N,
                                             int max_blocks, int window);
 
+/*
+ * What stands around the mixer in a stack: a lighter recurrent layer, the norm between layers, and
+ * the verification of drafted tokens that says how many of them a pool of states commits.
+ */
+
+/*
+ * The diagonal gated recurrence (the mixer's with one key channel and no erase: a state per
+ * channel), over whole sequences:
+ *     h_t = exp(log_alpha_t) h_{t-1} + w_t v_t,   o_t = h_t
+ *
+ *   v, log_alpha, w : [B, T, D] (dtype). Token t (of B * T) starts at element t * stride of its own,
+ *                     its channels dense, so they may be slices of one projection; strides are at
+ *                     least D and multiples of 8. w may be NULL (ones). log_alpha <= 0; -inf (a
+ *                     reset) is fine.
+ *   initial_state   : [N, D] fp32, or NULL for zeros
+ *   o               : dense [B, T, D] (dtype), written; may be NULL where only states are wanted
+ *   final_state     : [N, D] fp32, or NULL; may be initial_state
+ *   states          : NULL, or gdn2_linear_recurrence_states_bytes(...) bytes: the states before
+ *                     every 64th token, which the backward reads
+ *   cu_seqlens      : as for gdn2_chunk_fwd. Rows in front of the first packed sequence and behind
+ *                     the last are not written.
+ *   Supported: D a multiple of 8, both dtypes. A NaN or an infinity stays in its own sequence and
+ *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 is a no-op.
+ * Returns GDN2_OK or an error status.
+ */
+int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
+                           const float* initial_state, void* o, float* final_state, float* states,
+                           const int32_t* cu_seqlens, int B, int T, int D, int N,
+                           int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
+                           void* hip_stream);
+size_t gdn2_linear_recurrence_states_bytes(int packed, int B, int T, int D, int N);
+
+/*
+ * Gradients of gdn2_linear_recurrence: dv, dlog_alpha, dw (dense, dtype; dw only with w) and
+ * d_initial_state ([N, D] fp32, or NULL) from d_o (dense), d_final_state ([N, D] fp32, or NULL for
+ * zeros), the inputs and the states that the forward kept for them. Rows that belong to no packed
+ * sequence get zeros. Equal inputs give equal bits. Returns GDN2_OK or an error status.
+ */
+int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void* w,
+                               const float* states, const void* d_o, const float* d_final_state,
+                               void* dv, void* dlog_alpha, void* dw, float* d_initial_state,
+                               const int32_t* cu_seqlens, int B, int T, int D, int N,
+                               int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
+                               void* hip_stream);
+
+/*
+ * L consecutive tokens of each of N sequences against a pool of states, as gdn2_decode_tokens is
+ * for the mixer: v, log_alpha, w [N, L, D] with strides as above (w may be NULL), state_pool
+ * [P, D] fp32, o and step_states (fp32, or NULL) dense [N, L, D]; state_indices, commit_len and
+ * what they mean as there. Returns GDN2_OK or an error status.
+ */
+int gdn2_linear_recurrence_tokens(const void* v, const void* log_alpha, const void* w,
+                                  float* state_pool, const int32_t* state_indices,
+                                  const int32_t* commit_len, void* o, float* step_states, int N,
+                                  int L, int D, int P, int64_t v_stride, int64_t g_stride,
+                                  int64_t w_stride, int dtype, void* hip_stream);
+
+/*
+ * The norm between layers, with the residual's addition:
+ *     h = x + residual   (rounded to the residual's type: the stream that the next layer adds to)
+ *     y = h / sqrt(mean(h^2) + eps) * weight     (of h as it is stored; fp32 inside)
+ *
+ *   x        : [rows, D] (dtype), row i at element i * x_stride, channels dense
+ *   residual : [rows, D] (r_dtype), r_stride likewise; or NULL: h = x, and h is not written
+ *   weight   : [D] fp32
+ *   y        : dense [rows, D] (dtype); with scale, e4m3 codes (bytes)
+ *   h        : dense [rows, D] (r_dtype); may be residual, or x, where that is dense and of its type
+ *   scale    : NULL, or fp32 [rows, D / group] (group 0: [rows], one a row): the value of a code is
+ *              e4m3 * scale, with scale the smallest power of two s >= 2^-64 with max|y| <= 448 s over
+ *              its group. A row with a NaN or an infinity gives NaN codes where y is NaN.
+ *   group    : 0, 32, 64 or 128 channels (0 without scale); D a multiple of it
+ *   Supported: D a multiple of 8 up to 16384; types bf16 with bf16, bf16 with an fp32 residual, fp32
+ *   with fp32. Magnitudes below 2^63, past which the mean square leaves fp32. rows = 0 is a no-op.
+ * Returns GDN2_OK or an error status.
+ */
+int gdn2_residual_norm(const void* x, const void* residual, const float* weight, void* y, void* h,
+                       float* scale, int64_t rows, int D, int64_t x_stride, int64_t r_stride,
+                       int group, float eps, int dtype, int r_dtype, void* hip_stream);
+
+/*
+ * Gradients of gdn2_residual_norm without scale: from dy (dtype) and dh (r_dtype, or NULL for zero),
+ * both dense, and h as the forward wrote it (h_stride: x itself where there was no residual),
+ *     dh_total = dh + rho (u - n mean(u n)),  n = h rho,  u = dy weight
+ * to dx (dtype) and, where the types differ, to dr (r_dtype; else NULL), and dweight [D] fp32. dx
+ * may be dy, or dh where the types agree. Sums over rows are formed in a fixed order.
+ *   workspace : at least gdn2_residual_norm_bwd_workspace_bytes(rows, D) bytes, 16-byte aligned
+ * rows = 0 is a no-op (dweight is not written). Returns GDN2_OK or an error status.
+ */
+int gdn2_residual_norm_bwd(const void* dy, const void* dh, const void* h, const float* weight,
+                           void* dx, void* dr, float* dweight, int64_t rows, int D,
+                           int64_t h_stride, float eps, int dtype, int r_dtype, void* workspace,
+                           size_t workspace_bytes, void* hip_stream);
+size_t gdn2_residual_norm_bwd_workspace_bytes(int64_t rows, int D);
+
+/*
+ * Verification of drafted tokens from given random numbers. Sequence n has draft_len[n] drafts; p_i
+ * is the target's distribution in front of draft i (p behind the last draft at i = draft_len), q_i
+ * the draft's:
+ *     draft i is accepted where u_i q_i(x_i) < p_i(x_i) and all before it were;  a: how many were
+ *     the next token is drawn from max(p_a - q_a, 0) where draft a was rejected (from p_a where that
+ *     is zero everywhere), from p_a where none was: the first j whose cumulated weight passes
+ *     u_L times their sum (fp64)
+ * Rows need not sum to one. Entries that are not positive count as zero, NaN among them.
+ *
+ *   target_probs : [N, L + 1, V] (dtype), dense
+ *   draft_probs  : [N, L, V] (dtype), dense; or NULL: drafts that were certain (q(x_i) = 1)
+ *   drafts       : device int32 [N, L]; one outside [0, V) is rejected
+ *   draft_len    : device int32 [N], clamped to [0, L], or NULL for L
+ *   uniforms     : fp32 [N, L + 1] in [0, 1)
+ *   tokens       : int32 [N, L + 1], written: the accepted drafts, the next token, -1 behind it (the
+ *                  next token itself is -1 where p_a is zero everywhere)
+ *   commit_len   : int32 [N], written: a + 1. Of the L + 1 tokens that went through the target (the
+ *                  last one known, then the drafts), so many are to be kept: the commit_len of
+ *                  gdn2_decode_tokens and gdn2_linear_recurrence_tokens.
+ *   workspace    : at least gdn2_verify_drafts_workspace_bytes(N, V) bytes, 16-byte aligned; calls
+ *                  that can overlap need one each
+ *   N = 0 is a no-op. Returns GDN2_OK or an error status.
+ */
+int gdn2_verify_drafts(const void* target_probs, const void* draft_probs, const int32_t* drafts,
+                       const int32_t* draft_len, const float* uniforms, int32_t* tokens,
+                       int32_t* commit_len, int N, int L, int V, int dtype, void* workspace,
+                       size_t workspace_bytes, void* hip_stream);
+size_t gdn2_verify_drafts_workspace_bytes(int N, int V);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char* gdn2_status_string(int status);
 

@@ -1,0 +1,308 @@
+"""GPU tests of the diagonal gated recurrence (forward, backward, autograd, tokens against a pool)
+against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn2_stack as R
+from tests.attn_util import assert_within, draw, f64
+from tests.gpu_util import say
+from tests.stack_util import recurrence_bounds, recurrence_grad_bounds
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _case(seed, B, T, D, dt, gate=True, start=True, lens=None, strided=False, decay=0.3, tail=0):
+    """Inputs on the device and in float64. lens: a packed batch; tail: rows behind its last sequence."""
+    rng = np.random.default_rng(seed)
+    dtype = DT[dt]
+    cu = None
+    if lens is not None:
+        B, T, cu = 1, int(sum(lens)) + tail, np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    x = draw(rng, B, T, 3 * D + 8, dtype=torch.float32)
+    x[..., D:2 * D] = -decay * torch.nn.functional.softplus(x[..., D:2 * D])
+    x[..., 2 * D:3 * D] = torch.sigmoid(x[..., 2 * D:3 * D])
+    x = x.to(dtype).cuda()
+    v, g, w = (x[..., k * D:(k + 1) * D] for k in range(3))
+    if not strided:
+        v, g, w = (t.contiguous() for t in (v, g, w))
+    N = B if cu is None else len(lens)
+    s0 = torch.from_numpy(rng.standard_normal((N, D)).astype(np.float32)).cuda() if start else None
+    return v, g, w if gate else None, s0, cu, rng
+
+
+def _np(t):
+    return None if t is None else f64(t)
+
+
+def _cu(cu):
+    return None if cu is None else torch.from_numpy(cu).cuda()
+
+
+# B, T, D, dtype, gate, start, lens, strided, decay, tail
+CASES = [
+    (2, 37, 64, "bf16", True, True, None, False, 0.3, 0),
+    (1, 1, 8, "bf16", True, True, None, False, 0.3, 0),
+    (3, 2, 72, "fp32", True, False, None, True, 0.3, 0),
+    (1, 64, 136, "fp32", False, True, None, False, 0.3, 0),
+    (2, 65, 64, "fp32", True, True, None, True, 0.01, 0),
+    (1, 129, 200, "bf16", False, False, None, True, 0.01, 0),
+    (2, 128, 128, "bf16", True, True, None, False, 3.0, 0),
+    (1, 1000, 64, "bf16", True, True, None, False, 0.001, 0),
+    (1, 777, 24, "fp32", True, True, None, False, 0.001, 0),
+    (1, 0, 64, "bf16", True, True, [1, 0, 64, 63, 0, 130, 128, 2], False, 0.3, 0),
+    (1, 0, 104, "fp32", False, True, [0, 0, 65, 1, 200, 0], True, 0.1, 0),
+    (1, 0, 64, "bf16", True, False, [33, 300, 5], True, 0.1, 70),
+    (40, 3, 16, "fp32", True, True, None, False, 0.3, 0),
+]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_forward(case):
+    import gated_delta_rule_36_amd as G
+    B, T, D, dt, gate, start, lens, strided, decay, tail = case
+    v, g, w, s0, cu, _ = _case(7, B, T, D, dt, gate, start, lens, strided, decay, tail)
+    say("linear_recurrence_fwd", case)
+    o, last = G.linear_recurrence_fwd(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))
+    torch.cuda.synchronize()
+    assert o.dtype == DT[dt] and o.is_contiguous()
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(f64(v), f64(g), _np(w), _np(s0), cu, DT[dt])
+    end = ref.shape[1] - tail
+    assert_within("o", o[:, :end], ref[:, :end], bound[:, :end])
+    assert_within("final", last, lref, lbound)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_backward(case):
+    import gated_delta_rule_36_amd as G
+    B, T, D, dt, gate, start, lens, strided, decay, tail = case
+    v, g, w, s0, cu, rng = _case(8, B, T, D, dt, gate, start, lens, strided, decay, tail)
+    do = draw(rng, *v.shape, dtype=DT[dt]).cuda()
+    N = len(lens) if lens is not None else B
+    ds = torch.from_numpy(rng.standard_normal((N, D)).astype(np.float32)).cuda() if start else None
+    say("linear_recurrence_bwd", case)
+    o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))
+    got = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=ds, cu_seqlens=_cu(cu))
+    plain, _ = G.linear_recurrence_fwd(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))
+    torch.cuda.synchronize()
+    end = v.shape[1] - tail
+    assert torch.equal(o[:, :end], plain[:, :end])
+    ref = recurrence_grad_bounds(f64(v), f64(g), _np(w), f64(do), _np(s0), _np(ds), cu, DT[dt])
+    got = [x for x in got if x is not None]
+    assert len(got) == len(ref)
+    for name, x, (r, bound) in zip(("dv", "dg", "dw", "ds0") if gate else ("dv", "dg", "ds0"), got, ref):
+        assert_within(name, x, r, bound)
+    if tail:
+        assert not got[0][:, end:].any() and not got[1][:, end:].any()
+
+
+def test_resets_and_empty_batches():
+    """log alpha of -inf drops the state, gradients included; no tokens hand the state through."""
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, _, rng = _case(9, 2, 200, 64, "fp32")
+    g[:, ::17] = float("-inf")
+    g[1, 100:, 5] = -200.0
+    do = draw(rng, *v.shape, dtype=torch.float32).cuda()
+    say("linear_recurrence resets")
+    o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
+    grads = G.linear_recurrence_bwd(v, g, w, states, do)
+    torch.cuda.synchronize()
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, torch.float32)
+    assert_within("o", o, ref, bound)
+    assert_within("last", last, lref, lbound)
+    for x, (r, b) in zip(grads, recurrence_grad_bounds(f64(v), f64(g), f64(w), f64(do), f64(s0), None, None, torch.float32)):
+        assert_within("gradient", x, r, b)
+    assert not grads[1][:, ::17].any() and not grads[3].any()
+    e = torch.empty(2, 0, 64, device="cuda")
+    o, last, states = G.linear_recurrence_fwd_train(e, e, e, initial_state=s0)
+    assert o.shape == e.shape and torch.equal(last, s0)
+    ds = torch.randn_like(s0)
+    assert torch.equal(G.linear_recurrence_bwd(e, e, e, states, e, d_final_state=ds)[3], ds)
+    n = torch.empty(0, 5, 64, device="cuda")
+    assert G.linear_recurrence_fwd(n, n)[1].shape == (0, 64)
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    one = torch.randn(1, 70, 64, device="cuda")
+    o, last, states = G.linear_recurrence_fwd_train(one, -one.abs(), None, cu_seqlens=cu)
+    dv, dg, _, ds0 = G.linear_recurrence_bwd(one, -one.abs(), None, states, one, cu_seqlens=cu)
+    assert last.shape == ds0.shape == (0, 64) and not dv.any() and not dg.any()
+
+
+def test_bad_values_stay_in_their_sequence_and_channel():
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, cu, rng = _case(10, 1, 0, 72, "bf16", lens=[70, 200, 0, 31])
+    do = draw(rng, *v.shape).cuda()
+
+    def run():
+        o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))
+        return (o, last, *G.linear_recurrence_bwd(v, g, w, states, do, cu_seqlens=_cu(cu)))
+
+    say("linear_recurrence NaN and infinity")
+    good = run()
+    v[0, 100, 3] = float("nan")   # second sequence, token 30
+    v[0, 20, 70] = float("inf")   # first
+    got = run()
+    torch.cuda.synchronize()
+    touched = torch.zeros(301, 72, dtype=torch.bool, device="cuda")
+    touched[100:270, 3] = touched[20:70, 70] = True
+    assert got[0][0][touched].isfinite().sum() == 0
+    assert torch.equal(got[0][0][~touched], good[0][0][~touched])
+    last = torch.zeros(4, 72, dtype=torch.bool, device="cuda")
+    last[1, 3] = last[0, 70] = True
+    assert torch.equal(got[1][~last], good[1][~last]) and not got[1][last].isfinite().any()
+    assert torch.equal(got[2], good[2])  # dv does not read v
+    for k in (3, 4):                     # dg, dw: what comes before is not touched
+        assert torch.equal(got[k][0][~touched], good[k][0][~touched])
+
+
+def test_final_state_in_place_and_repeatable():
+    """The final states into the initial ones' memory; equal calls give equal bits."""
+    import gated_delta_rule_36_amd as G
+    from gated_delta_rule_36_amd import _attn
+    v, g, w, s0, _, rng = _case(11, 5, 333, 264, "bf16")
+    do = draw(rng, *v.shape).cuda()
+    say("linear_recurrence in place, twice")
+    runs = []
+    for _ in range(2):
+        o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
+        runs.append((o, last, *G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=last)))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    s, o = s0.clone(), torch.empty_like(v)
+    _attn._call("gdn2_linear_recurrence", v.device, v.data_ptr(), g.data_ptr(), w.data_ptr(), s.data_ptr(), o.data_ptr(),
+                s.data_ptr(), None, None, 5, 333, 264, 5, 264, 264, 264, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(s, runs[0][1]) and torch.equal(o, runs[0][0])
+
+
+def test_long_memory():
+    """A state that lives for thousands of tokens, the same decay at each of them: roundings of the
+    decay add up."""
+    import gated_delta_rule_36_amd as G
+    T = 20000
+    v = torch.zeros(1, T, 64, device="cuda")
+    g = torch.full_like(v, -1e-4) * torch.linspace(0.5, 1.5, 64, device="cuda")
+    s0 = torch.ones(1, 64, device="cuda")
+    say("linear_recurrence 20000 tokens of one decay")
+    o, last = G.linear_recurrence_fwd(v, g, initial_state=s0)
+    torch.cuda.synchronize()
+    ref = np.exp(np.cumsum(f64(g)[0], 0))
+    # one rounding of a run's decay (2 tokens: 2 U, |g| negligible) and one product for each run, and
+    # the runs' products: at most 5 U every 2 tokens
+    bound = 2.5 * 2.0 ** -24 * np.arange(1, T + 1)[:, None] * ref + 1e-6 * ref
+    assert_within("o", o[0], ref, bound)
+
+
+def test_autograd_equals_the_calls():
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, cu, rng = _case(13, 1, 0, 40, "fp32", lens=[5, 0, 90], strided=True)
+    do, ds = draw(rng, *v.shape, dtype=torch.float32).cuda(), torch.randn(3, 40, device="cuda")
+    say("linear_recurrence autograd")
+    leaves = [t.detach().clone().requires_grad_() for t in (v, g, w, s0)]
+    y = G.linear_recurrence(*leaves, cu_seqlens=_cu(cu))
+    torch.autograd.backward(y, (do, ds))
+    states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))[2]
+    ref = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=ds, cu_seqlens=_cu(cu))
+    torch.cuda.synchronize()
+    for leaf, r in zip(leaves, ref):
+        assert torch.equal(leaf.grad, r)
+    # slices of one leaf, an expanded gradient, one output only
+    x = torch.randn(1, 95, 128, device="cuda").requires_grad_()
+    o, _ = G.linear_recurrence(x[..., :40], -x[..., 40:80].abs(), x[..., 80:120])
+    o.sum().backward()
+    xs = f64(x)
+    (dv, _), (dg, _), (dw, _), _ = recurrence_grad_bounds(xs[..., :40], -np.abs(xs[..., 40:80]), xs[..., 80:120],
+                                                          np.ones((1, 95, 40)), None, None, None, torch.float32)
+    ref = np.concatenate([dv, -np.sign(xs[..., 40:80]) * dg, dw, 0 * xs[..., 120:]], -1)
+    assert np.abs(f64(x.grad) - ref).max() < 1e-4 * np.abs(ref).max()
+    (gg,) = torch.autograd.grad(G.linear_recurrence(x[..., :40], x[..., 40:80])[0].sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gg.square().sum().backward()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,L,D,gate", [(1, 1, 8, True), (7, 1, 200, False), (5, 5, 64, True), (300, 9, 24, True), (33, 4, 136, False)])
+def test_tokens(dt, N, L, D, gate):
+    import gated_delta_rule_36_amd as G
+    v, g, w, _, _, rng = _case(N + L, N, L, D, dt, gate, strided=L > 4)
+    P = N + 4
+    pool = torch.from_numpy(rng.standard_normal((P, D)).astype(np.float32)).cuda()
+    before = f64(pool)
+    idx = rng.permutation(P)[:N].astype(np.int32)
+    commit = rng.integers(-1, L + 2, N).astype(np.int32)
+    if N > 3:
+        idx[1], idx[2] = -1, P
+    say("linear_recurrence_tokens", dt, N, L, D, gate)
+    o, steps = G.linear_recurrence_tokens(v, g, w, pool, state_indices=torch.from_numpy(idx).cuda(),
+                                          commit_len=torch.from_numpy(commit).cuda(), return_step_states=True)
+    torch.cuda.synchronize()
+    ok = (idx >= 0) & (idx < P)
+    vn, gn, wn = f64(v)[ok], f64(g)[ok], None if w is None else f64(w)[ok]
+    ref, bound, _, _, m, e = recurrence_bounds(vn, gn, wn, before[idx[ok]], None, DT[dt])
+    okt = torch.from_numpy(ok).cuda()
+    assert_within("o", o[okt], ref, bound)
+    assert_within("steps", steps[okt], ref, e + 2.0 ** -24 * np.abs(ref) + 1e-38)
+    _, _, after = R.recurrence_tokens(before, f64(v), f64(g), _np(w), idx, commit)
+    wide = np.zeros((P, D))
+    for n, k in enumerate(np.flatnonzero(ok)):
+        c = min(max(commit[k], 0), L)
+        if c:
+            wide[idx[k]] = e[n, c - 1] + 2.0 ** -24 * np.abs(after[idx[k]]) + 1e-38
+    assert_within("pool", pool, after, wide)
+
+
+def test_tokens_equal_the_forward():
+    """Slots in order, everything committed; twice in a row is one longer call."""
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, _, _ = _case(14, 6, 10, 64, "fp32")
+    say("linear_recurrence_tokens after each other")
+    pool = s0.clone()
+    a, _ = G.linear_recurrence_tokens(*(t[:, :4].contiguous() for t in (v, g, w)), pool)
+    b, steps = G.linear_recurrence_tokens(*(t[:, 4:].contiguous() for t in (v, g, w)), pool)
+    ref, last = G.linear_recurrence_fwd(v, g, w, initial_state=s0)
+    torch.cuda.synchronize()
+    assert steps is None
+    r, bound, lr, lbound, _, _ = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, torch.float32)
+    assert_within("o", torch.cat([a, b], 1), r, bound)
+    assert_within("pool", pool, lr, lbound)
+
+
+def test_capture_replay_and_another_stream():
+    """Forward, backward and tokens in one graph, replayed on new inputs; a call on a side stream."""
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, _, rng = _case(15, 2, 150, 64, "bf16")
+    do, pool = draw(rng, *v.shape).cuda(), torch.randn(2, 64, device="cuda")
+    say("linear_recurrence capture")
+
+    three = [t[:, :3].contiguous() for t in (v, g, w)]
+
+    def all_of():
+        o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
+        p = pool.clone()
+        t, _ = G.linear_recurrence_tokens(*three, p)
+        return (o, last, *G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=last), t, p)
+
+    ref = all_of()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        other = all_of()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = all_of()
+    for seed in range(3):
+        r = np.random.default_rng(seed)
+        v.copy_(draw(r, *v.shape))
+        do.copy_(draw(r, *do.shape))
+        s0.normal_()
+        ref = all_of()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, ref))
