@@ -94,11 +94,14 @@ def lib():
         L.gdn2_cache_attention.restype = _I
         L.gdn2_cache_attention_workspace_bytes.argtypes = [_I] * 9
         L.gdn2_cache_attention_workspace_bytes.restype = _Z
-        L.gdn2_linear_recurrence.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P]
+        L.gdn2_linear_recurrence.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P, _Z, _P]
         L.gdn2_linear_recurrence.restype = _I
         L.gdn2_linear_recurrence_states_bytes.argtypes = [_I] * 5
         L.gdn2_linear_recurrence_states_bytes.restype = _Z
-        L.gdn2_linear_recurrence_bwd.argtypes = [_P] * 11 + [_I] * 4 + [_I64] * 3 + [_I, _P]
+        L.gdn2_linear_recurrence_bwd.argtypes = ([_P] * 11 + [_I] * 4 + [_I64] * 3 +
+                                                 [_I, _P, _Z, _P])
+        L.gdn2_linear_recurrence_workspace_bytes.argtypes = [_I] * 5
+        L.gdn2_linear_recurrence_workspace_bytes.restype = _Z
         L.gdn2_linear_recurrence_bwd.restype = _I
         L.gdn2_linear_recurrence_tokens.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P]
         L.gdn2_linear_recurrence_tokens.restype = _I

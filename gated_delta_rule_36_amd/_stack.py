@@ -74,18 +74,25 @@ def _recurrence_args(v, g, w, cu_seqlens):
     return B, T, D, N, strides, code, dev, dt
 
 
+@functools.lru_cache(maxsize=1024)
+def _recurrence_sizes(packed, B, T, D, N):
+    """Workspace bytes of a call, and slots of its kept states."""
+    L = lib()
+    return (int(L.gdn2_linear_recurrence_workspace_bytes(packed, B, T, D, N)),
+            int(L.gdn2_linear_recurrence_states_bytes(packed, B, T, D, N)) // (4 * D))
+
+
 def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
     B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
     if initial_state is not None:
         _dense("initial_state", initial_state, (N, D), torch.float32, dev)
     o = _empty(v)
     last = torch.empty((N, D), dtype=torch.float32, device=dev) if output_final_state else None
-    states = None
-    if keep:
-        need = lib().gdn2_linear_recurrence_states_bytes(cu_seqlens is not None, B, T, D, N)
-        states = torch.empty((need // (4 * D), D), dtype=torch.float32, device=dev)
+    need, slots = _recurrence_sizes(cu_seqlens is not None, B, T, D, N)
+    states = torch.empty((slots, D), dtype=torch.float32, device=dev) if keep else None
+    ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence", dev, v.data_ptr(), g.data_ptr(), _p(w), _p(initial_state),
-          o.data_ptr(), _p(last), _p(states), _p(cu_seqlens), B, T, D, N, *strides, code)
+          o.data_ptr(), _p(last), _p(states), _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
     return o, last, states
 
 
@@ -117,16 +124,17 @@ def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=No
     d_final_state: fp32 [N, D] or None. Rows that belong to no packed sequence get zeros."""
     B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
     _dense("do", do, (B, T, D), dt, dev)
-    slots = lib().gdn2_linear_recurrence_states_bytes(cu_seqlens is not None, B, T, D, N) // (4 * D)
+    need, slots = _recurrence_sizes(cu_seqlens is not None, B, T, D, N)
     _dense("states", states, (slots, D), torch.float32, dev)
     if d_final_state is not None:
         _dense("d_final_state", d_final_state, (N, D), torch.float32, dev)
     dv, dg = torch.empty_like(do), torch.empty_like(do)
     dw = None if w is None else torch.empty_like(do)
     ds0 = torch.empty((N, D), dtype=torch.float32, device=dev)
+    ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence_bwd", dev, v.data_ptr(), g.data_ptr(), _p(w), states.data_ptr(),
           do.data_ptr(), _p(d_final_state), dv.data_ptr(), dg.data_ptr(), _p(dw), ds0.data_ptr(),
-          _p(cu_seqlens), B, T, D, N, *strides, code)
+          _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
     return dv, dg, dw, ds0
 
 

@@ -35,7 +35,8 @@ int check_recurrence(const void* v, const void* g, const void* w, const int32_t*
   if (D % 8 != 0) return GDN2_UNSUPPORTED;
   if (!stride_ok(v_stride, D) || !stride_ok(g_stride, D) || (w != nullptr && !stride_ok(w_stride, D)))
     return GDN2_INVALID_ARGUMENT;
-  if ((long)B * T > (long)INT_MAX || gdn2::recurrence_groups(N, D) > (long)INT_MAX)
+  if ((long)B * T > (long)INT_MAX - 4096) return GDN2_INVALID_ARGUMENT;
+  if (gdn2::recurrence_groups(gdn2::recurrence_cut(cu_seqlens != nullptr, B, T, D, N), D) > (long)INT_MAX)
     return GDN2_INVALID_ARGUMENT;
   if ((long)B * T > 0 && (!v || !g)) return GDN2_INVALID_ARGUMENT;
   if (!all_aligned16({v, g, w}) || !aligned(cu_seqlens, 4)) return GDN2_INVALID_ARGUMENT;
@@ -43,13 +44,15 @@ int check_recurrence(const void* v, const void* g, const void* w, const int32_t*
 }
 
 gdn2::RecurrenceArgs recurrence_args(const void* v, const void* g, const void* w,
-                                     const int32_t* cu_seqlens, int T, int D, int N,
+                                     const int32_t* cu_seqlens, int B, int T, int D, int N,
                                      int64_t v_stride, int64_t g_stride, int64_t w_stride,
-                                     int dtype, void* stream) {
+                                     int dtype, void* workspace, void* stream) {
   gdn2::RecurrenceArgs a{};
   a.v = v; a.g = g; a.w = w; a.cu_seqlens = cu_seqlens;
   a.v_stride = v_stride; a.g_stride = g_stride; a.w_stride = w_stride;
   a.T = T; a.N = N; a.D = D; a.dtype = dtype; a.stream = stream;
+  a.cut = gdn2::recurrence_cut(cu_seqlens != nullptr, B, T, D, N);
+  a.cut.maps = static_cast<float*>(workspace);
   return a;
 }
 
@@ -67,6 +70,13 @@ int check_norm(int64_t rows, int D, float eps, int dtype, int r_dtype) {
 
 extern "C" {
 
+size_t gdn2_linear_recurrence_workspace_bytes(int packed, int B, int T, int D, int N) {
+  if (B < 0 || T < 0 || D <= 0 || D % 8 != 0 || N < 0 || (packed ? B != 1 : N != B) ||
+      (long)B * T > (long)INT_MAX - 4096)
+    return 0;
+  return gdn2::recurrence_workspace_bytes(gdn2::recurrence_cut(packed != 0, B, T, D, N), D);
+}
+
 size_t gdn2_linear_recurrence_states_bytes(int packed, int B, int T, int D, int N) {
   if (B < 0 || T < 0 || D <= 0 || D % 8 != 0 || N < 0 || (packed ? B != 1 : N != B)) return 0;
   return (size_t)gdn2::recurrence_state_slots(packed != 0, B, T, N) * D * sizeof(float);
@@ -76,15 +86,17 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
                            const float* initial_state, void* o, float* final_state, float* states,
                            const int32_t* cu_seqlens, int B, int T, int D, int N,
                            int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
-                           void* hip_stream) {
+                           void* workspace, size_t workspace_bytes, void* hip_stream) {
   const int st = check_recurrence(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
                                   w_stride, dtype);
   if (st != GDN2_OK) return st;
   if ((long)B * T > 0 && !o && !states) return GDN2_INVALID_ARGUMENT;
-  if (!all_aligned16({initial_state, o, final_state, states})) return GDN2_INVALID_ARGUMENT;
+  if (!all_aligned16({initial_state, o, final_state, states, workspace})) return GDN2_INVALID_ARGUMENT;
   if (N == 0) return GDN2_OK;
-  gdn2::RecurrenceArgs a = recurrence_args(v, log_alpha, w, cu_seqlens, T, D, N, v_stride,
-                                           g_stride, w_stride, dtype, hip_stream);
+  const size_t need = gdn2_linear_recurrence_workspace_bytes(cu_seqlens != nullptr, B, T, D, N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
+  gdn2::RecurrenceArgs a = recurrence_args(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride,
+                                           g_stride, w_stride, dtype, workspace, hip_stream);
   a.s0 = initial_state; a.o = o; a.sN = final_state; a.states = states;
   return status_of(gdn2::launch_recurrence(a));
 }
@@ -94,18 +106,21 @@ int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void*
                                void* dv, void* dlog_alpha, void* dw, float* d_initial_state,
                                const int32_t* cu_seqlens, int B, int T, int D, int N,
                                int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
-                               void* hip_stream) {
+                               void* workspace, size_t workspace_bytes, void* hip_stream) {
   const int st = check_recurrence(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
                                   w_stride, dtype);
   if (st != GDN2_OK) return st;
   if ((long)B * T > 0 && (!states || !d_o || !dv || !dlog_alpha || (w != nullptr && !dw)))
     return GDN2_INVALID_ARGUMENT;
-  if (!all_aligned16({states, d_o, d_final_state, dv, dlog_alpha, dw, d_initial_state}))
+  if (!all_aligned16({states, d_o, d_final_state, dv, dlog_alpha, dw, d_initial_state,
+                      workspace}))
     return GDN2_INVALID_ARGUMENT;
   if (N == 0 && (long)B * T == 0) return GDN2_OK;
+  const size_t need = gdn2_linear_recurrence_workspace_bytes(cu_seqlens != nullptr, B, T, D, N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
   gdn2::RecurrenceBwdArgs b{};
-  b.f = recurrence_args(v, log_alpha, w, cu_seqlens, T, D, N, v_stride, g_stride, w_stride, dtype,
-                        hip_stream);
+  b.f = recurrence_args(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride, w_stride,
+                        dtype, workspace, hip_stream);
   b.f.states = const_cast<float*>(states);
   b.d_o = d_o; b.d_sN = d_final_state;
   b.dv = dv; b.dg = dlog_alpha; b.dw = dw; b.d_s0 = d_initial_state;

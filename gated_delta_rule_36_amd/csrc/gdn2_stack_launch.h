@@ -10,6 +10,15 @@
 namespace gdn2 {
 
 // ---- diagonal recurrence: h = exp(g) h + w v, a state per channel
+
+// How sequences are cut: into units of seg tokens.
+struct RecurrenceCut {
+  bool cut;          // some sequence may have more than one unit
+  int seg;           // tokens of a unit
+  int per_sequence;  // units of a sequence (packed batches: see the kernels)
+  int units;
+  float* maps;       // workspace [units, 2, D], where cut
+};
 struct RecurrenceArgs {
   const void *v, *g, *w;      // [tokens, D], rows dense, one stride each; w may be null (ones)
   const float* s0;            // [N, D] or null
@@ -19,6 +28,7 @@ struct RecurrenceArgs {
   const int32_t* cu_seqlens;  // [N + 1] or null
   long v_stride, g_stride, w_stride;
   int T, N, D, dtype;         // T: tokens of a sequence, or in all when packed
+  RecurrenceCut cut;
   void* stream;
 };
 struct RecurrenceBwdArgs {
@@ -43,7 +53,9 @@ struct RecurrenceTokensArgs {
 // n * ceil(T / kStateTokens), packed at cu_seqlens[n] / kStateTokens + n.
 constexpr int kStateTokens = 64;
 long recurrence_state_slots(bool packed, int B, int T, int N);
-long recurrence_groups(int N, int D);  // workgroups of the largest launch
+RecurrenceCut recurrence_cut(bool packed, int B, int T, int D, int N);
+long recurrence_groups(const RecurrenceCut& c, int D);  // workgroups of the largest launch
+size_t recurrence_workspace_bytes(const RecurrenceCut& c, int D);
 hipError_t launch_recurrence(const RecurrenceArgs& a);
 hipError_t launch_recurrence_bwd(const RecurrenceBwdArgs& a);
 hipError_t launch_recurrence_tokens(const RecurrenceTokensArgs& a);

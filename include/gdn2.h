@@ -525,7 +525,11 @@ size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, in
  *                     every 64th token, which the backward reads
  *   cu_seqlens      : as for gdn2_chunk_fwd. Rows in front of the first packed sequence and behind
  *                     the last are not written.
- *   Supported: D a multiple of 8, both dtypes. A NaN or an infinity stays in its own sequence and
+ *   workspace       : at least gdn2_linear_recurrence_workspace_bytes(...) bytes (0: may be NULL),
+ *                     16-byte aligned, free for the call's duration on `hip_stream`; calls that can
+ *                     overlap, captured ones among them, need one each. Long sequences of few
+ *                     channels are cut into segments that run in parallel.
+ *   Supported: D a multiple of 8, both dtypes, B * T below 2^31 - 4096. A NaN or an infinity stays in its own sequence and
  *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 is a no-op.
  * Returns GDN2_OK or an error status.
  */
@@ -533,13 +537,14 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
                            const float* initial_state, void* o, float* final_state, float* states,
                            const int32_t* cu_seqlens, int B, int T, int D, int N,
                            int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
-                           void* hip_stream);
+                           void* workspace, size_t workspace_bytes, void* hip_stream);
+size_t gdn2_linear_recurrence_workspace_bytes(int packed, int B, int T, int D, int N);
 size_t gdn2_linear_recurrence_states_bytes(int packed, int B, int T, int D, int N);
 
 /*
  * Gradients of gdn2_linear_recurrence: dv, dlog_alpha, dw (dense, dtype; dw only with w) and
  * d_initial_state ([N, D] fp32, or NULL) from d_o (dense), d_final_state ([N, D] fp32, or NULL for
- * zeros), the inputs and the states that the forward kept for them. Rows that belong to no packed
+ * zeros), the inputs and the states that the forward kept for them; workspace as for the forward. Rows that belong to no packed
  * sequence get zeros. Equal inputs give equal bits. Returns GDN2_OK or an error status.
  */
 int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void* w,
@@ -547,7 +552,7 @@ int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void*
                                void* dv, void* dlog_alpha, void* dw, float* d_initial_state,
                                const int32_t* cu_seqlens, int B, int T, int D, int N,
                                int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
-                               void* hip_stream);
+                               void* workspace, size_t workspace_bytes, void* hip_stream);
 
 /*
  * L consecutive tokens of each of N sequences against a pool of states, as gdn2_decode_tokens is

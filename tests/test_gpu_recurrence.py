@@ -61,6 +61,13 @@ CASES = [
     (1, 0, 104, "fp32", False, True, [0, 0, 65, 1, 200, 0], True, 0.1, 0),
     (1, 0, 64, "bf16", True, False, [33, 300, 5], True, 0.1, 70),
     (40, 3, 16, "fp32", True, True, None, False, 0.3, 0),
+    # cut into segments: the last one whole, of one token, of one tile; packed, with empty sequences,
+    # sequences that end at a segment's end and behind it, rows behind the last
+    (1, 2048, 64, "bf16", True, True, None, False, 0.01, 0),
+    (2, 1537, 72, "fp32", True, True, None, True, 0.01, 0),
+    (1, 9000, 8, "fp32", False, False, None, False, 0.001, 0),
+    (1, 0, 64, "bf16", True, True, [256, 0, 1025, 1, 512, 257], False, 0.01, 0),
+    (1, 0, 136, "fp32", True, True, [3000, 0, 7], True, 0.01, 300),
 ]
 
 
@@ -175,7 +182,7 @@ def test_final_state_in_place_and_repeatable():
     assert all(torch.equal(a, b) for a, b in zip(*runs))
     s, o = s0.clone(), torch.empty_like(v)
     _attn._call("gdn2_linear_recurrence", v.device, v.data_ptr(), g.data_ptr(), w.data_ptr(), s.data_ptr(), o.data_ptr(),
-                s.data_ptr(), None, None, 5, 333, 264, 5, 264, 264, 264, 0)
+                s.data_ptr(), None, None, 5, 333, 264, 5, 264, 264, 264, 0, None, 0)
     torch.cuda.synchronize()
     assert torch.equal(s, runs[0][1]) and torch.equal(o, runs[0][0])
 

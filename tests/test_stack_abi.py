@@ -17,11 +17,11 @@ M2 = 0x100002
 
 
 def _rec(what, **kw):
-    a = dict(v=F, g=F, w=F, s0=F, o=F, sN=F, st=F, cu=None, do=F, ds=F, dv=F, dg=F, dw=F, d0=F, B=2, T=8, D=64, N=2,
+    a = dict(v=F, g=F, w=F, s0=F, o=F, sN=F, st=F, cu=None, do=F, ds=F, dv=F, dg=F, dw=F, d0=F, B=2, T=8, D=64, N=2, ws_=F, wsz=1 << 30,
              vs=64, gs=64, ws=64, dtype=0, pool=F, idx=None, com=None, steps=None, L=3, P=2)
     a.update(kw)
     L = _lib.lib()
-    tail = [a["vs"], a["gs"], a["ws"], a["dtype"], None]
+    tail = [a["vs"], a["gs"], a["ws"], a["dtype"], a["ws_"], a["wsz"], None]
     if what == "fwd":
         return L.gdn2_linear_recurrence(a["v"], a["g"], a["w"], a["s0"], a["o"], a["sN"], a["st"], a["cu"], a["B"],
                                         a["T"], a["D"], a["N"], *tail)
@@ -29,7 +29,7 @@ def _rec(what, **kw):
         return L.gdn2_linear_recurrence_bwd(a["v"], a["g"], a["w"], a["st"], a["do"], a["ds"], a["dv"], a["dg"], a["dw"],
                                             a["d0"], a["cu"], a["B"], a["T"], a["D"], a["N"], *tail)
     return L.gdn2_linear_recurrence_tokens(a["v"], a["g"], a["w"], a["pool"], a["idx"], a["com"], a["o"], a["steps"],
-                                           a["N"], a["L"], a["D"], a["P"], *tail)
+                                           a["N"], a["L"], a["D"], a["P"], *tail[:4], None)
 
 
 @pytest.mark.parametrize("what", ["fwd", "bwd", "tokens"])
@@ -55,6 +55,24 @@ def test_recurrence_refusals(what):
     assert _rec(what, B=0, N=0, T=0, **none) == 0
     if what == "tokens":
         assert _rec(what, L=0, **none) == 0
+
+
+@pytest.mark.parametrize("what", ["fwd", "bwd"])
+def test_recurrence_workspace(what):
+    """One long sequence of few channels is cut into segments, which need room for their maps; many
+    sequences, short ones, none are not."""
+    ask = _lib.lib().gdn2_linear_recurrence_workspace_bytes
+    need = ask(0, 1, 5000, 64, 1)
+    assert need == 20 * 2 * 64 * 4  # 20 segments of 256 tokens
+    one = dict(B=1, N=1, T=5000)
+    assert _rec(what, ws_=None, **one) == 3
+    assert _rec(what, wsz=need - 1, **one) == 3
+    assert _rec(what, ws_=M4, **one) == 1
+    assert ask(0, 1, 700, 64, 1) == ask(0, 200, 5000, 64, 200) == ask(0, 1, 5000, 64, 2) == ask(0, 1, 5000, 60, 1) == 0
+    assert ask(1, 1, 5000, 64, 3) == (5000 // 256 + 3) * 2 * 64 * 4
+    # packed batches of many sequences: one of them may be much longer than the others
+    assert ask(1, 1, 200000, 64, 200) == (200000 // 1024 + 200) * 2 * 64 * 4
+    assert ask(0, 1, -1, 64, 1) == ask(0, 1, (1 << 31) - 1, 64, 1) == 0
 
 
 def test_recurrence_states():
