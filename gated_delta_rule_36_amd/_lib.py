@@ -100,7 +100,7 @@ def lib():
         L.gdn2_linear_recurrence_states_bytes.restype = _Z
         L.gdn2_linear_recurrence_bwd.argtypes = ([_P] * 11 + [_I] * 4 + [_I64] * 3 +
                                                  [_I, _P, _Z, _P])
-        L.gdn2_linear_recurrence_workspace_bytes.argtypes = [_I] * 5
+        L.gdn2_linear_recurrence_workspace_bytes.argtypes = [_I] * 6
         L.gdn2_linear_recurrence_workspace_bytes.restype = _Z
         L.gdn2_linear_recurrence_bwd.restype = _I
         L.gdn2_linear_recurrence_tokens.argtypes = [_P] * 8 + [_I] * 4 + [_I64] * 3 + [_I, _P]

@@ -75,10 +75,10 @@ def _recurrence_args(v, g, w, cu_seqlens):
 
 
 @functools.lru_cache(maxsize=1024)
-def _recurrence_sizes(packed, B, T, D, N):
+def _recurrence_sizes(backward, packed, B, T, D, N):
     """Workspace bytes of a call, and slots of its kept states."""
     L = lib()
-    return (int(L.gdn2_linear_recurrence_workspace_bytes(packed, B, T, D, N)),
+    return (int(L.gdn2_linear_recurrence_workspace_bytes(backward, packed, B, T, D, N)),
             int(L.gdn2_linear_recurrence_states_bytes(packed, B, T, D, N)) // (4 * D))
 
 
@@ -88,7 +88,7 @@ def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
         _dense("initial_state", initial_state, (N, D), torch.float32, dev)
     o = _empty(v)
     last = torch.empty((N, D), dtype=torch.float32, device=dev) if output_final_state else None
-    need, slots = _recurrence_sizes(cu_seqlens is not None, B, T, D, N)
+    need, slots = _recurrence_sizes(False, cu_seqlens is not None, B, T, D, N)
     states = torch.empty((slots, D), dtype=torch.float32, device=dev) if keep else None
     ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence", dev, v.data_ptr(), g.data_ptr(), _p(w), _p(initial_state),
@@ -124,7 +124,7 @@ def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=No
     d_final_state: fp32 [N, D] or None. Rows that belong to no packed sequence get zeros."""
     B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
     _dense("do", do, (B, T, D), dt, dev)
-    need, slots = _recurrence_sizes(cu_seqlens is not None, B, T, D, N)
+    need, slots = _recurrence_sizes(True, cu_seqlens is not None, B, T, D, N)
     _dense("states", states, (slots, D), torch.float32, dev)
     if d_final_state is not None:
         _dense("d_final_state", d_final_state, (N, D), torch.float32, dev)

@@ -23,7 +23,7 @@ namespace gdn2 {
 namespace {
 
 constexpr int kStrip = 64;   // channels of a workgroup
-constexpr int kRuns = 32;    // runs of a tile: 4 waves x 8
+constexpr int kRuns = 32;    // runs of 4 waves
 
 template <typename T> constexpr int run_tokens() { return sizeof(T) == 2 ? 4 : 2; }
 
@@ -141,17 +141,17 @@ __device__ __forceinline__ void scan_level_both(int lane, float* A, float* H, fl
   }
 }
 
-// x through the maps of segments [s0, s1) of a sequence whose units begin at `unit`, in every lane of
-// x's channels: the 32 runs take some segments each, in the order of time (BACK: against it).
-// s_map: [A, H][wave][channel].
-template <bool BACK>
+// x, a value of the lane's own channel `c` of the strip, through the maps of segments [s0, s1) of a
+// sequence whose units begin at `unit`: the runs take some segments each, in the order of time (BACK:
+// against it). s_map: [A, H][wave][channel].
+template <bool BACK, int NW>
 __device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit, int s0, int s1, int chl, int lane,
-                                              int run, float* s_map, float* x) {
+                                              int run, int c, float* s_map, float& x) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), cg = lane & 7;
-  const int each = (s1 - s0 + kRuns - 1) / kRuns;
+  const int each = (s1 - s0 + NW * 8 - 1) / (NW * 8);
   float A[8], H[8], XA[8], XH[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) A[c] = XA[c] = 1.f, H[c] = XH[c] = 0.f;
+  for (int j = 0; j < 8; ++j) A[j] = XA[j] = 1.f, H[j] = XH[j] = 0.f;
   for (int i = 0; i < each; ++i) {
     const int k = run * each + i;
     if (k >= s1 - s0) break;
@@ -160,9 +160,9 @@ __device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit,
     load8f(m, ma);
     load8f(m + a.D, mh);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      A[c] *= ma[c];
-      H[c] = fmaf(ma[c], H[c], mh[c]);
+    for (int j = 0; j < 8; ++j) {
+      A[j] *= ma[j];
+      H[j] = fmaf(ma[j], H[j], mh[j]);
     }
   }
   scan_level<8>(lane, A, H, XA, XH);
@@ -170,17 +170,11 @@ __device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit,
   scan_level<32>(lane, A, H, XA, XH);
   if (lane < 8) {
     store8(s_map + wave * kStrip + cg * 8, A);
-    store8(s_map + (4 + wave) * kStrip + cg * 8, H);
+    store8(s_map + (NW + wave) * kStrip + cg * 8, H);
   }
   lds_barrier();
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float wa[8], wh[8];
-    load8f(s_map + u * kStrip + cg * 8, wa);
-    load8f(s_map + (4 + u) * kStrip + cg * 8, wh);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = fmaf(wa[c], x[c], wh[c]);
-  }
+  for (int u = 0; u < NW; ++u) x = fmaf(s_map[u * kStrip + c], x, s_map[(NW + u) * kStrip + c]);
 }
 
 // A tile's inputs as loaded: R tokens of 8 channels.
@@ -189,55 +183,88 @@ struct Raw {
   Vec8<T> x[ARRAYS][R];
 };
 
+// Eight channels that are read once: past the caches' retention.
+__device__ __forceinline__ void load_stream(Vec8<bf16>& r, const bf16* p) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  r.r = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)));
+}
+__device__ __forceinline__ void load_stream(Vec8<float>& r, const float* p) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  r.r0 = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)));
+  r.r1 = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p) + 1));
+}
+
 }  // namespace
 
-// One workgroup a (unit, 64 channels).
-template <typename T, bool GATE>
-__global__ void __launch_bounds__(256) gdn2_recurrence_kernel(RecurrenceArgs a, int unit0) {
-  constexpr int R = run_tokens<T>(), TILE = kRuns * R, NA = GATE ? 3 : 2;
-  __shared__ __attribute__((aligned(16))) float s_map[2][2][4][kStrip];  // [parity][A, H][wave][channel]
+// Rows t0 + row of up to ARRAYS inputs: a uniform base and one 32-bit offset a lane (strides are at most
+// kMaxStride, so that the rows of a tile stay within it).
+template <typename T, int ARRAYS>
+struct Rows {
+  const T* src[ARRAYS];  // uniform: the strip's first channel in the sequence's first row
+  long stride[ARRAYS];
+  int ch;                // the lane's channel in the strip
+  template <int R>
+  __device__ __forceinline__ void load(Raw<T, R, ARRAYS>& r, int t0, int row0, int rows) const {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k) {
+        const int i = (j + k) % R;
+        const int row = row0 + i < rows ? row0 + i : rows - 1;
+        load_stream(r.x[k][i], src[k] + t0 * stride[k] + ((unsigned)__umul24(row, (int)stride[k]) + ch));
+      }
+    }
+  }
+};
+
+// One workgroup a (unit, 64 channels). A tile's registers are filled with the next tile's inputs as
+// soon as its values are widened to fp32, so that loads are in flight during the scan and the stores.
+template <typename T, bool GATE, int NW>
+__global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs a) {
+  constexpr int R = run_tokens<T>(), TILE = NW * 8 * R, NA = GATE ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) float s_map[2][2][NW][kStrip];  // [parity][A, H][wave][channel]
+  __shared__ __attribute__((aligned(16))) float s_in[NW][kStrip];         // the state before a wave's runs
   const int strips = (a.D + kStrip - 1) / kStrip;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = unit0 + blockIdx.x / strips;
+  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
   const Piece p = piece_of(a, unit);
   if (p.begin > p.end) return;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
-  const int ch = (blockIdx.x % strips) * kStrip + cg * 8;
+  const int ch = strip + cg * 8;
   const bool live = ch < a.D;
   const int chl = live ? ch : a.D - 8;  // lanes past the channels load some of the last ones
-  const T* src[3] = {(const T*)a.v + chl, (const T*)a.g + chl, GATE ? (const T*)a.w + chl : nullptr};
-  const long stride[3] = {a.v_stride, a.g_stride, a.w_stride};
+  // the channel whose state this lane carries from tile to tile
+  const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
+  Rows<T, NA> in;
+  in.src[0] = (const T*)a.v + p.first * a.v_stride + strip;
+  in.src[1] = (const T*)a.g + p.first * a.g_stride + strip;
+  in.stride[0] = a.v_stride;
+  in.stride[1] = a.g_stride;
+  if constexpr (GATE) {
+    in.src[2] = (const T*)a.w + p.first * a.w_stride + strip;
+    in.stride[2] = a.w_stride;
+  }
+  in.ch = chl - strip;
+  T* const out = a.o != nullptr ? (T*)a.o + p.first * a.D + strip : nullptr;
+  float* const kept = a.states != nullptr ? a.states + p.slot * a.D + ch : nullptr;
 
-  auto load = [&](Raw<T, R, NA>& r, int t0) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      int t = t0 + run * R + i;
-      t = t < p.end ? t : p.end - 1;
-#pragma unroll
-      for (int k = 0; k < NA; ++k) r.x[k][i].load(src[k] + (p.first + t) * stride[k]);
-    }
-  };
-  Raw<T, R, NA> cur, next;
-  if (p.begin < p.end) load(cur, p.begin);
-  // The state before the tile, in every lane of its channels. The initial one goes through LDS from
-  // the lanes that write the final one, which may be the same memory.
-  float h[8] = {};
+  Raw<T, R, NA> r;
+  if (p.begin < p.end) in.load(r, p.begin, run * R, p.end - p.begin);
+  // The initial state goes through LDS from the lanes that write the final one, which may be the same
+  // memory.
+  float h = 0.f;
   if (a.s0 != nullptr) {
-    if (threadIdx.x < 8) {
-      load8f(a.s0 + (long)p.n * a.D + chl, h);
-      store8(&s_map[1][0][0][cg * 8], h);
-    }
+    if (wave == 0) s_map[1][0][0][own] = a.s0[(long)p.n * a.D + och];
     lds_barrier();
-    load8f(&s_map[1][0][0][cg * 8], h);
+    h = s_map[1][0][0][own];
   }
   int parity = 0;
   if (p.index > 0) {  // the maps of the segments before this one
-    fold_segments<false>(a, unit - p.index, 0, p.index, chl, lane, run, &s_map[0][0][0][0], h);
+    fold_segments<false, NW>(a, unit - p.index, 0, p.index, chl, lane, run, own, &s_map[0][0][0][0], h);
     parity = 1;
   }
   for (int t0 = p.begin; t0 < p.end; t0 += TILE) {
-    if (t0 + TILE < p.end) load(next, t0 + TILE);
     const int mine = p.end - (t0 + run * R);  // tokens of this run, from R down to none
     float al[R][8], z[R][8], A[8], H[8], XA[8], XH[8];
 #pragma unroll
@@ -245,9 +272,9 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_kernel(RecurrenceArgs a, 
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float w[8], g[8];
-      cur.x[0][i].to_float(z[i]);
-      cur.x[1][i].to_float(g);
-      if constexpr (GATE) cur.x[2][i].to_float(w);
+      r.x[0][i].to_float(z[i]);
+      r.x[1][i].to_float(g);
+      if constexpr (GATE) r.x[2][i].to_float(w);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         if constexpr (GATE) z[i][c] *= w[c];
@@ -258,6 +285,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_kernel(RecurrenceArgs a, 
         H[c] = fmaf(al[i][c], H[c], z[i][c]);
       }
     }
+    if (t0 + TILE < p.end) in.load(r, t0 + TILE, run * R, p.end - t0 - TILE);
 #pragma unroll
     for (int c = 0; c < 8; ++c) A[c] = fast_exp2(A[c]);
     scan_level<8>(lane, A, H, XA, XH);
@@ -268,35 +296,33 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_kernel(RecurrenceArgs a, 
       store8(&s_map[parity][1][wave][cg * 8], H);
     }
     lds_barrier();
-    float x[8];  // the state before this wave's runs, then before this lane's
+    // each lane joins the waves' maps for its own channel and hands the state before this wave's runs
+    // to the lanes that hold the channel
+    float xin = h;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float wa[8], wh[8];
-      load8f(&s_map[parity][0][u][cg * 8], wa);
-      load8f(&s_map[parity][1][u][cg * 8], wh);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (u == wave) x[c] = h[c];
-        h[c] = fmaf(wa[c], h[c], wh[c]);
-      }
+    for (int u = 0; u < NW; ++u) {
+      if (u == wave) xin = h;
+      h = fmaf(s_map[parity][0][u][own], h, s_map[parity][1][u][own]);
     }
+    s_in[wave][own] = xin;
     parity ^= 1;
+    float x[8];
+    load8f(&s_in[wave][cg * 8], x);
 #pragma unroll
     for (int c = 0; c < 8; ++c) x[c] = fmaf(XA[c], x[c], XH[c]);
     const int t = t0 + run * R;
-    if (a.states != nullptr && live && mine > 0 && t % kStateTokens == 0)
-      store8(a.states + (p.slot + t / kStateTokens) * a.D + ch, x);
-    if (a.o != nullptr) {
+    if (kept != nullptr && live && mine > 0 && t % kStateTokens == 0) store8(kept + (long)(t / kStateTokens) * a.D, x);
+    if (out != nullptr) {
+      T* const to = out + (long)t0 * a.D;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = fmaf(al[i][c], x[c], z[i][c]);
-        if (live && i < mine) store8_stream((T*)a.o + (p.first + t + i) * a.D + ch, x);
+        if (live && i < mine) store8_stream(to + ((unsigned)__umul24(run * R + i, a.D) + cg * 8), x);
       }
     }
-    cur = next;
   }
-  if (a.sN != nullptr && p.end == p.len && live && threadIdx.x < 8) store8(a.sN + (long)p.n * a.D + ch, h);
+  if (a.sN != nullptr && p.end == p.len && wave == 0 && strip + own < a.D) a.sN[(long)p.n * a.D + och] = h;
 }
 
 // The maps of the segments of long sequences, which run in parallel where sequences and channels
@@ -304,15 +330,15 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_kernel(RecurrenceArgs a, 
 // e -> A e + L of every segment behind another. A lane walks seg / 32 consecutive tokens of 8
 // channels; the 32 runs are joined through LDS.
 template <typename T, bool GATE, bool BACK>
-__global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArgs a, const T* d_o, int unit0) {
+__global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArgs a, const T* d_o) {
   constexpr int AHEAD = 4, NA = !BACK && GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][kRuns][kStrip];
   const int strips = (a.D + kStrip - 1) / kStrip;
-  const int unit = unit0 + blockIdx.x / strips;
+  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
   const Piece p = piece_of(a, unit);
   if (p.begin >= p.end || (BACK ? p.begin == 0 : p.end == p.len)) return;
   const int cg = threadIdx.x & 7, run = threadIdx.x >> 3;
-  const int ch = (blockIdx.x % strips) * kStrip + cg * 8;
+  const int ch = strip + cg * 8;
   const int chl = ch < a.D ? ch : a.D - 8;
   const T* src[3] = {(const T*)a.g + chl, BACK ? d_o + chl : (const T*)a.v + chl, GATE ? (const T*)a.w + chl : nullptr};
   const long stride[3] = {a.g_stride, BACK ? (long)a.D : a.v_stride, a.w_stride};
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
   store8(&s_map[1][run][cg * 8], H);
   lds_barrier();
   if (threadIdx.x < kStrip) {
-    const int c = (blockIdx.x % strips) * kStrip + threadIdx.x;
+    const int c = strip + threadIdx.x;
     float A = 1.f, B = 0.f;
 #pragma unroll 8
     for (int k = 0; k < kRuns; ++k) {
@@ -377,26 +403,28 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
 }
 
 // Gradients, tiles from the last to the first: the states come from the kept ones, the carry e runs
-// against time. One more workgroup row behind the sequences (packed batches) writes zeros to the
-// gradients of rows that belong to none.
-template <typename T, bool GATE>
-__global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdArgs b, int unit0) {
-  constexpr int R = 2, TILE = kRuns * R, NA = GATE ? 4 : 3;
-  static_assert(TILE == kStateTokens, "a tile starts at a kept state");
-  __shared__ __attribute__((aligned(16))) float s_map[2][3][4][kStrip];  // [parity][A, H, L][wave][channel]
+// against time. One more workgroup row behind the units (packed batches) writes zeros to the
+// gradients of rows that belong to no sequence.
+template <typename T, bool GATE, int NW>
+__global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(RecurrenceBwdArgs b) {
+  constexpr int R = 2, TILE = NW * 8 * R, NA = GATE ? 4 : 3;
+  static_assert(TILE % kStateTokens == 0, "a tile starts at a kept state");
+  __shared__ __attribute__((aligned(16))) float s_map[2][3][NW][kStrip];  // [parity][A, H, L][wave][channel]
+  __shared__ __attribute__((aligned(16))) float s_in[2][NW][kStrip];      // the state before a wave's runs, the gradient behind
   const RecurrenceArgs& a = b.f;
   const int strips = (a.D + kStrip - 1) / kStrip;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = unit0 + blockIdx.x / strips;
+  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
-  const int ch = (blockIdx.x % strips) * kStrip + cg * 8;
+  const int ch = strip + cg * 8;
   const bool live = ch < a.D;
   const int chl = live ? ch : a.D - 8;
+  const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
   if (unit == a.cut.units) {
     const int first = clamped_offset(a.cu_seqlens, 0, a.T), last = clamped_offset(a.cu_seqlens, a.N, a.T);
     const float zero[8] = {};
-    for (int t = run; t < a.T; t += kRuns)
+    for (int t = run; t < a.T; t += NW * 8)
       if (live && (t < first || t >= last)) {
         store8((T*)b.dv + (long)t * a.D + ch, zero);
         store8((T*)b.dg + (long)t * a.D + ch, zero);
@@ -406,47 +434,54 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdA
   }
   const Piece p = piece_of(a, unit);
   if (p.begin > p.end) return;
-  const T* src[4] = {(const T*)a.v + chl, (const T*)a.g + chl, (const T*)b.d_o + chl, GATE ? (const T*)a.w + chl : nullptr};
-  const long stride[4] = {a.v_stride, a.g_stride, (long)a.D, a.w_stride};
+  Rows<T, NA> in;
+  in.src[0] = (const T*)a.v + p.first * a.v_stride + strip;
+  in.src[1] = (const T*)a.g + p.first * a.g_stride + strip;
+  in.src[2] = (const T*)b.d_o + p.first * a.D + strip;
+  in.stride[0] = a.v_stride;
+  in.stride[1] = a.g_stride;
+  in.stride[2] = a.D;
+  if constexpr (GATE) {
+    in.src[3] = (const T*)a.w + p.first * a.w_stride + strip;
+    in.stride[3] = a.w_stride;
+  }
+  in.ch = chl - strip;
+  const float* const kept = a.states + p.slot * a.D + och;
+  const long out = p.first * a.D + strip;
 
-  float e[8];  // the gradient of the state behind the tile, in every lane of its channels
-#pragma unroll
-  for (int c = 0; c < 8; ++c) e[c] = 0.f;
-  if (b.d_sN != nullptr) load8f(b.d_sN + (long)p.n * a.D + chl, e);
+  // of the lane's own channel: the gradient of the state behind the tile, the state before it
+  float e = b.d_sN != nullptr ? b.d_sN[(long)p.n * a.D + och] : 0.f, hnext = 0.f;
   int parity = 0;
-
-  auto load = [&](Raw<T, R, NA>& r, float* h, int t0) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      int t = t0 + run * R + i;
-      t = t < p.end ? t : p.end - 1;
-#pragma unroll
-      for (int k = 0; k < NA; ++k) r.x[k][i].load(src[k] + (p.first + t) * stride[k]);
-    }
-    load8f(a.states + (p.slot + t0 / kStateTokens) * a.D + chl, h);
+  Raw<T, R, NA> r;
+  auto load = [&](int t0) {
+    in.load(r, t0, run * R, p.end - t0);
+    hnext = kept[(long)(t0 / kStateTokens) * a.D];
   };
-  Raw<T, R, NA> cur, next;
-  float h[8], hnext[8];
   const int t_last = p.begin + (p.end - 1 - p.begin) / TILE * TILE;
-  if (p.begin < p.end) load(cur, h, t_last);
+  if (p.begin < p.end) load(t_last);
   if (p.end < p.len) {  // the maps of the segments behind this one
     const int count = (p.len + a.cut.seg - 1) / a.cut.seg;
-    fold_segments<true>(a, unit - p.index, p.index + 1, count, chl, lane, run, &s_map[0][0][0][0], e);
+    fold_segments<true, NW>(a, unit - p.index, p.index + 1, count, chl, lane, run, own, &s_map[0][0][0][0], e);
     parity = 1;
   }
   for (int t0 = t_last; p.begin < p.end && t0 >= p.begin; t0 -= TILE) {
-    if (t0 > p.begin) load(next, hnext, t0 - TILE);
     const int mine = p.end - (t0 + run * R);
+    Vec8<T> rv[R], rw[R];
     float al[R][8], z[R][8], d[R][8], A[8], H[8], L[8], XA[8], XH[8], XB[8], XL[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) A[c] = H[c] = L[c] = XH[c] = XL[c] = 0.f, XA[c] = XB[c] = 1.f;
+    float h = hnext;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float w[8], g[8];
-      cur.x[0][i].to_float(z[i]);
-      cur.x[1][i].to_float(g);
-      cur.x[2][i].to_float(d[i]);
-      if constexpr (GATE) cur.x[3][i].to_float(w);
+      rv[i] = r.x[0][i];
+      rv[i].to_float(z[i]);
+      r.x[1][i].to_float(g);
+      r.x[2][i].to_float(d[i]);
+      if constexpr (GATE) {
+        rw[i] = r.x[3][i];
+        rw[i].to_float(w);
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         if constexpr (GATE) z[i][c] *= w[c];
@@ -457,6 +492,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdA
         H[c] = fmaf(al[i][c], H[c], z[i][c]);
       }
     }
+    if (t0 > p.begin) load(t0 - TILE);
 #pragma unroll
     for (int i = R - 1; i >= 0; --i)
 #pragma unroll
@@ -472,22 +508,22 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdA
       store8(&s_map[parity][2][wave][cg * 8], L);
     }
     lds_barrier();
-    float x[8], y[8];  // the state before this lane's run, the gradient behind it
+    float xin = h, yin = e;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float wa[8], wh[8], ba[8], bl[8];
-      load8f(&s_map[parity][0][u][cg * 8], wa);
-      load8f(&s_map[parity][1][u][cg * 8], wh);
-      load8f(&s_map[parity][0][3 - u][cg * 8], ba);
-      load8f(&s_map[parity][2][3 - u][cg * 8], bl);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (u == wave) x[c] = h[c];
-        h[c] = fmaf(wa[c], h[c], wh[c]);
-        if (3 - u == wave) y[c] = e[c];
-        e[c] = fmaf(ba[c], e[c], bl[c]);
-      }
+    for (int u = 0; u < NW; ++u) {
+      if (u == wave) xin = h;
+      h = fmaf(s_map[parity][0][u][own], h, s_map[parity][1][u][own]);
     }
+#pragma unroll
+    for (int u = NW - 1; u >= 0; --u) {
+      if (u == wave) yin = e;
+      e = fmaf(s_map[parity][0][u][own], e, s_map[parity][2][u][own]);
+    }
+    s_in[0][wave][own] = xin;
+    s_in[1][wave][own] = yin;
+    float x[8], y[8];  // the state before this lane's run, the gradient behind it
+    load8f(&s_in[0][wave][cg * 8], x);
+    load8f(&s_in[1][wave][cg * 8], y);
     parity ^= 1;
     float before[R][8];
 #pragma unroll
@@ -502,11 +538,12 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdA
         before[i][c] = x[c];
         x[c] = fmaf(al[i][c], x[c], z[i][c]);
       }
+    const long at0 = out + (long)t0 * a.D;
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
       float v[8], w[8], gv[8], gg[8], gw[8];
-      cur.x[0][i].to_float(v);
-      if constexpr (GATE) cur.x[3][i].to_float(w);
+      rv[i].to_float(v);
+      if constexpr (GATE) rw[i].to_float(w);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const float dt = d[i][c] + y[c];
@@ -516,17 +553,14 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_bwd_kernel(RecurrenceBwdA
         gg[c] = y[c] * before[i][c];
       }
       if (live && i < mine) {
-        const long at = (p.first + t0 + run * R + i) * a.D + ch;
-        store8_stream((T*)b.dv + at, gv);
-        store8_stream((T*)b.dg + at, gg);
-        if constexpr (GATE) store8_stream((T*)b.dw + at, gw);
+        const unsigned at = (unsigned)__umul24(run * R + i, a.D) + cg * 8;
+        store8_stream((T*)b.dv + at0 + at, gv);
+        store8_stream((T*)b.dg + at0 + at, gg);
+        if constexpr (GATE) store8_stream((T*)b.dw + at0 + at, gw);
       }
     }
-    cur = next;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) h[c] = hnext[c];
   }
-  if (b.d_s0 != nullptr && p.begin == 0 && live && threadIdx.x < 8) store8(b.d_s0 + (long)p.n * a.D + ch, e);
+  if (b.d_s0 != nullptr && p.begin == 0 && wave == 0 && strip + own < a.D) b.d_s0[(long)p.n * a.D + och] = e;
 }
 
 // L tokens of every sequence against a pool of states: a lane takes 8 channels of one sequence, its
@@ -582,21 +616,31 @@ long recurrence_state_slots(bool packed, int B, int T, int N) {
 
 static int strips_of(int D) { return (D + kStrip - 1) / kStrip; }
 
-RecurrenceCut recurrence_cut(bool packed, int B, int T, int D, int N) {
+// A unit takes a workgroup for each of its strips, and a compute unit holds two workgroups. Uncut,
+// units are sequences: with few of them most of the card stands idle; cut, the maps' pass reads the
+// inputs once more (6 of 8 + 6 bytes an element forward, 4 of 14 + 4 backward). Measured at 2048
+// channels in bf16, 4096 tokens, forward and backward in us:
+//   sequences                 1          2          3          4          5          6
+//   uncut                 69, 140    69, 141    72, 146    76, 150    86, 158    98, 170
+//   cut                   26,  34    46,  61    66,  90    89, 112   108, 150   129, 175
+// Where workgroups run past a whole round of the card (9 sequences, 288: 80 and 145 uncut, 84 and 120
+// cut) the last round counts like a full one: cut where less than 0.44 (0.66) of the rounds is used.
+// Packed batches, whose lengths the host does not know, are cut at twice the fair share in any case,
+// for a sequence much longer than the others.
+RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, int N) {
   constexpr int TILE = 128;
   RecurrenceCut c{};
-  const long strips = strips_of(D), tokens = (long)B * T;
-  c.cut = false;
+  const long strips = strips_of(D), tokens = (long)B * T, groups = N * strips;
   c.seg = T > 0 ? T : 1;
   c.per_sequence = 1;
   c.units = N;
-  if (T < 6 * TILE || N == 0) return c;
-  // tokens of a unit where everything is cut into 512 of (unit, strip), two for a compute unit
-  long seg = ((tokens * strips + 511) / 512 + TILE - 1) / TILE * TILE;
+  if (T < (backward ? 3 : 6) * TILE || N == 0) return c;
+  long seg = ((tokens * strips + 1023) / 1024 + TILE - 1) / TILE * TILE;  // the fair share
   if (seg < 2 * TILE) seg = 2 * TILE;
-  if (N * strips > 96) {
+  const long rounds = (groups + 255) / 256;
+  if (groups * 100 >= rounds * 256 * (backward ? 66 : 44)) {
     if (!packed) return c;
-    seg *= 2;
+    seg *= 4;  // of 512 workgroups
   }
   if (seg >= T) return c;
   c.cut = true;
@@ -612,24 +656,37 @@ size_t recurrence_workspace_bytes(const RecurrenceCut& c, int D) {
 
 namespace {
 
+// Eight waves a workgroup (twice the tile) for whole sequences of up to two workgroups a compute unit:
+// 4 x 4096 tokens of 2048 channels 85 -> 76 us forward, 171 -> 150 backward; 64 x 256 53 -> 59. (The
+// backward in fp32 has no registers for it.)
+bool wide_groups(const RecurrenceCut& c, int strips) { return !c.cut && (long)c.units * strips <= 512; }
+
 template <typename T, bool GATE>
 hipError_t forward(const RecurrenceArgs& a) {
-  const unsigned strips = (unsigned)strips_of(a.D);
   const hipStream_t st = (hipStream_t)a.stream;
-  const dim3 grid((unsigned)a.cut.units * strips), block(256);
-  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), grid, block, 0, st, a, (const T*)nullptr, 0);
-  hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE>), grid, block, 0, st, a, 0);
+  const int strips = strips_of(a.D);
+  const dim3 grid((unsigned)(a.cut.units * strips));
+  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), grid, dim3(256), 0, st, a, (const T*)nullptr);
+  if (wide_groups(a.cut, strips)) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 template <typename T, bool GATE>
 hipError_t backward(const RecurrenceBwdArgs& b) {
   const RecurrenceArgs& a = b.f;
-  const unsigned strips = (unsigned)strips_of(a.D);
   const hipStream_t st = (hipStream_t)a.stream;
-  const unsigned units = (unsigned)a.cut.units;
-  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3(units * strips), dim3(256), 0, st, a, (const T*)b.d_o, 0);
-  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE>), dim3((units + (a.cu_seqlens != nullptr)) * strips), dim3(256), 0, st, b, 0);
+  const int strips = strips_of(a.D);
+  if (a.cut.cut)
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3((unsigned)(a.cut.units * strips)), dim3(256), 0, st, a, (const T*)b.d_o);
+  const dim3 grid((unsigned)((a.cut.units + (a.cu_seqlens != nullptr)) * strips));  // the last row: rows of no sequence
+  if constexpr (sizeof(T) == 2) {
+    if (wide_groups(a.cut, strips)) {
+      hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 8>), grid, dim3(512), 0, st, b);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 4>), grid, dim3(256), 0, st, b);
   return hipGetLastError();
 }
 

@@ -24,26 +24,29 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {
 }
 bool dtype_ok(int dtype) { return dtype == GDN2_BF16 || dtype == GDN2_F32; }
 bool stride_ok(int64_t stride, int D) { return stride >= D && stride % 8 == 0; }
+// (the recurrence's kernels keep a tile's offsets in 32 bits)
+bool token_stride_ok(int64_t stride, int D) { return stride_ok(stride, D) && stride <= gdn2::kMaxStride; }
 int status_of(hipError_t e) { return e == hipSuccess ? GDN2_OK : GDN2_LAUNCH_FAILED; }
 
 // Sizes, strides and inputs that the whole-sequence forward and backward share.
-int check_recurrence(const void* v, const void* g, const void* w, const int32_t* cu_seqlens, int B,
+int check_recurrence(bool backward, const void* v, const void* g, const void* w, const int32_t* cu_seqlens, int B,
                      int T, int D, int N, int64_t v_stride, int64_t g_stride, int64_t w_stride,
                      int dtype) {
   if (!dtype_ok(dtype) || B < 0 || T < 0 || D <= 0 || N < 0) return GDN2_INVALID_ARGUMENT;
   if (cu_seqlens == nullptr ? N != B : B != 1) return GDN2_INVALID_ARGUMENT;
   if (D % 8 != 0) return GDN2_UNSUPPORTED;
-  if (!stride_ok(v_stride, D) || !stride_ok(g_stride, D) || (w != nullptr && !stride_ok(w_stride, D)))
+  if (!token_stride_ok(v_stride, D) || !token_stride_ok(g_stride, D) ||
+      (w != nullptr && !token_stride_ok(w_stride, D)))
     return GDN2_INVALID_ARGUMENT;
   if ((long)B * T > (long)INT_MAX - 4096) return GDN2_INVALID_ARGUMENT;
-  if (gdn2::recurrence_groups(gdn2::recurrence_cut(cu_seqlens != nullptr, B, T, D, N), D) > (long)INT_MAX)
+  if (gdn2::recurrence_groups(gdn2::recurrence_cut(backward, cu_seqlens != nullptr, B, T, D, N), D) > (long)INT_MAX)
     return GDN2_INVALID_ARGUMENT;
   if ((long)B * T > 0 && (!v || !g)) return GDN2_INVALID_ARGUMENT;
   if (!all_aligned16({v, g, w}) || !aligned(cu_seqlens, 4)) return GDN2_INVALID_ARGUMENT;
   return GDN2_OK;
 }
 
-gdn2::RecurrenceArgs recurrence_args(const void* v, const void* g, const void* w,
+gdn2::RecurrenceArgs recurrence_args(bool backward, const void* v, const void* g, const void* w,
                                      const int32_t* cu_seqlens, int B, int T, int D, int N,
                                      int64_t v_stride, int64_t g_stride, int64_t w_stride,
                                      int dtype, void* workspace, void* stream) {
@@ -51,7 +54,7 @@ gdn2::RecurrenceArgs recurrence_args(const void* v, const void* g, const void* w
   a.v = v; a.g = g; a.w = w; a.cu_seqlens = cu_seqlens;
   a.v_stride = v_stride; a.g_stride = g_stride; a.w_stride = w_stride;
   a.T = T; a.N = N; a.D = D; a.dtype = dtype; a.stream = stream;
-  a.cut = gdn2::recurrence_cut(cu_seqlens != nullptr, B, T, D, N);
+  a.cut = gdn2::recurrence_cut(backward, cu_seqlens != nullptr, B, T, D, N);
   a.cut.maps = static_cast<float*>(workspace);
   return a;
 }
@@ -70,11 +73,11 @@ int check_norm(int64_t rows, int D, float eps, int dtype, int r_dtype) {
 
 extern "C" {
 
-size_t gdn2_linear_recurrence_workspace_bytes(int packed, int B, int T, int D, int N) {
+size_t gdn2_linear_recurrence_workspace_bytes(int backward, int packed, int B, int T, int D, int N) {
   if (B < 0 || T < 0 || D <= 0 || D % 8 != 0 || N < 0 || (packed ? B != 1 : N != B) ||
       (long)B * T > (long)INT_MAX - 4096)
     return 0;
-  return gdn2::recurrence_workspace_bytes(gdn2::recurrence_cut(packed != 0, B, T, D, N), D);
+  return gdn2::recurrence_workspace_bytes(gdn2::recurrence_cut(backward != 0, packed != 0, B, T, D, N), D);
 }
 
 size_t gdn2_linear_recurrence_states_bytes(int packed, int B, int T, int D, int N) {
@@ -87,15 +90,15 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
                            const int32_t* cu_seqlens, int B, int T, int D, int N,
                            int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
                            void* workspace, size_t workspace_bytes, void* hip_stream) {
-  const int st = check_recurrence(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
+  const int st = check_recurrence(false, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
                                   w_stride, dtype);
   if (st != GDN2_OK) return st;
   if ((long)B * T > 0 && !o && !states) return GDN2_INVALID_ARGUMENT;
   if (!all_aligned16({initial_state, o, final_state, states, workspace})) return GDN2_INVALID_ARGUMENT;
   if (N == 0) return GDN2_OK;
-  const size_t need = gdn2_linear_recurrence_workspace_bytes(cu_seqlens != nullptr, B, T, D, N);
+  const size_t need = gdn2_linear_recurrence_workspace_bytes(0, cu_seqlens != nullptr, B, T, D, N);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
-  gdn2::RecurrenceArgs a = recurrence_args(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride,
+  gdn2::RecurrenceArgs a = recurrence_args(false, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride,
                                            g_stride, w_stride, dtype, workspace, hip_stream);
   a.s0 = initial_state; a.o = o; a.sN = final_state; a.states = states;
   return status_of(gdn2::launch_recurrence(a));
@@ -107,7 +110,7 @@ int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void*
                                const int32_t* cu_seqlens, int B, int T, int D, int N,
                                int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
                                void* workspace, size_t workspace_bytes, void* hip_stream) {
-  const int st = check_recurrence(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
+  const int st = check_recurrence(true, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride,
                                   w_stride, dtype);
   if (st != GDN2_OK) return st;
   if ((long)B * T > 0 && (!states || !d_o || !dv || !dlog_alpha || (w != nullptr && !dw)))
@@ -116,10 +119,10 @@ int gdn2_linear_recurrence_bwd(const void* v, const void* log_alpha, const void*
                       workspace}))
     return GDN2_INVALID_ARGUMENT;
   if (N == 0 && (long)B * T == 0) return GDN2_OK;
-  const size_t need = gdn2_linear_recurrence_workspace_bytes(cu_seqlens != nullptr, B, T, D, N);
+  const size_t need = gdn2_linear_recurrence_workspace_bytes(1, cu_seqlens != nullptr, B, T, D, N);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
   gdn2::RecurrenceBwdArgs b{};
-  b.f = recurrence_args(v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride, w_stride,
+  b.f = recurrence_args(true, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride, g_stride, w_stride,
                         dtype, workspace, hip_stream);
   b.f.states = const_cast<float*>(states);
   b.d_o = d_o; b.d_sN = d_final_state;
@@ -134,7 +137,8 @@ int gdn2_linear_recurrence_tokens(const void* v, const void* log_alpha, const vo
                                   int64_t w_stride, int dtype, void* hip_stream) {
   if (!dtype_ok(dtype) || N < 0 || L < 0 || D <= 0 || P < 0) return GDN2_INVALID_ARGUMENT;
   if (D % 8 != 0) return GDN2_UNSUPPORTED;
-  if (!stride_ok(v_stride, D) || !stride_ok(g_stride, D) || (w != nullptr && !stride_ok(w_stride, D)))
+  if (!token_stride_ok(v_stride, D) || !token_stride_ok(g_stride, D) ||
+      (w != nullptr && !token_stride_ok(w_stride, D)))
     return GDN2_INVALID_ARGUMENT;
   if (N == 0 || L == 0) return GDN2_OK;
   if (!v || !log_alpha || !state_pool || !o) return GDN2_INVALID_ARGUMENT;

@@ -52,8 +52,9 @@ struct RecurrenceTokensArgs {
 // Kept states: one before every kStateTokens tokens of a sequence. Sequence n's begin at slot
 // n * ceil(T / kStateTokens), packed at cu_seqlens[n] / kStateTokens + n.
 constexpr int kStateTokens = 64;
+constexpr int kMaxStride = 1 << 21;  // elements from one token to the next
 long recurrence_state_slots(bool packed, int B, int T, int N);
-RecurrenceCut recurrence_cut(bool packed, int B, int T, int D, int N);
+RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, int N);
 long recurrence_groups(const RecurrenceCut& c, int D);  // workgroups of the largest launch
 size_t recurrence_workspace_bytes(const RecurrenceCut& c, int D);
 hipError_t launch_recurrence(const RecurrenceArgs& a);

@@ -516,7 +516,7 @@ size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, in
  *
  *   v, log_alpha, w : [B, T, D] (dtype). Token t (of B * T) starts at element t * stride of its own,
  *                     its channels dense, so they may be slices of one projection; strides are at
- *                     least D and multiples of 8. w may be NULL (ones). log_alpha <= 0; -inf (a
+ *                     least D, multiples of 8 and at most 2^21. w may be NULL (ones). log_alpha <= 0; -inf (a
  *                     reset) is fine.
  *   initial_state   : [N, D] fp32, or NULL for zeros
  *   o               : dense [B, T, D] (dtype), written; may be NULL where only states are wanted
@@ -538,7 +538,8 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
                            const int32_t* cu_seqlens, int B, int T, int D, int N,
                            int64_t v_stride, int64_t g_stride, int64_t w_stride, int dtype,
                            void* workspace, size_t workspace_bytes, void* hip_stream);
-size_t gdn2_linear_recurrence_workspace_bytes(int packed, int B, int T, int D, int N);
+/* backward: whether for gdn2_linear_recurrence_bwd; packed: whether cu_seqlens is given. */
+size_t gdn2_linear_recurrence_workspace_bytes(int backward, int packed, int B, int T, int D, int N);
 size_t gdn2_linear_recurrence_states_bytes(int packed, int B, int T, int D, int N);
 
 /*

@@ -35,7 +35,7 @@ def _rec(what, **kw):
 @pytest.mark.parametrize("what", ["fwd", "bwd", "tokens"])
 def test_recurrence_refusals(what):
     bad = [(1, dict(dtype=2)), (1, dict(dtype=-1)), (1, dict(N=-1)), (1, dict(D=0)), (1, dict(D=-8)), (2, dict(D=60)),
-           (1, dict(vs=56)), (1, dict(gs=68)), (1, dict(ws=0)), (1, dict(v=None)), (1, dict(g=None)), (1, dict(v=M4)),
+           (1, dict(vs=56)), (1, dict(gs=68)), (1, dict(ws=0)), (1, dict(vs=(1 << 21) + 8)), (1, dict(ws=1 << 32)), (1, dict(v=None)), (1, dict(g=None)), (1, dict(v=M4)),
            (1, dict(w=M4))]
     if what == "tokens":
         bad += [(1, dict(pool=None)), (1, dict(pool=M4)), (1, dict(o=None)), (1, dict(o=M4)), (1, dict(L=-1)), (1, dict(P=1)),
@@ -61,14 +61,17 @@ def test_recurrence_refusals(what):
 def test_recurrence_workspace(what):
     """One long sequence of few channels is cut into segments, which need room for their maps; many
     sequences, short ones, none are not."""
-    ask = _lib.lib().gdn2_linear_recurrence_workspace_bytes
+    back = what == "bwd"
+    ask = lambda *a: _lib.lib().gdn2_linear_recurrence_workspace_bytes(back, *a)  # noqa: E731
     need = ask(0, 1, 5000, 64, 1)
     assert need == 20 * 2 * 64 * 4  # 20 segments of 256 tokens
     one = dict(B=1, N=1, T=5000)
     assert _rec(what, ws_=None, **one) == 3
     assert _rec(what, wsz=need - 1, **one) == 3
     assert _rec(what, ws_=M4, **one) == 1
-    assert ask(0, 1, 700, 64, 1) == ask(0, 200, 5000, 64, 200) == ask(0, 1, 5000, 64, 2) == ask(0, 1, 5000, 60, 1) == 0
+    assert ask(0, 1, 300, 64, 1) == ask(0, 200, 5000, 64, 200) == ask(0, 1, 5000, 64, 2) == ask(0, 1, 5000, 60, 1) == 0
+    assert (ask(0, 1, 700, 64, 1) > 0) == back        # backward from 384 tokens, forward from 768
+    assert (ask(0, 140, 5000, 64, 140) > 0) == back   # and up to a larger part of the card
     assert ask(1, 1, 5000, 64, 3) == (5000 // 256 + 3) * 2 * 64 * 4
     # packed batches of many sequences: one of them may be much longer than the others
     assert ask(1, 1, 200000, 64, 200) == (200000 // 1024 + 200) * 2 * 64 * 4
