@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "gdn2_attn_device.h"
+#include "gdn2_stack_device.h"
 #include "gdn2_stack_launch.h"
 
 namespace gdn2 {
@@ -84,8 +85,8 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
   for (int e = 0; e < E; ++e) {
     const int ch = ((e * W + part) * 64 + lane) * 8;
     if (ch < a.D) {
-      rx[e].load(x + ch);
-      if constexpr (ADD) rr[e].load(r + ch);
+      load_stream(rx[e], x + ch);
+      if constexpr (ADD) load_stream(rr[e], r + ch);
     }
   }
   float h[E][8];
@@ -201,9 +202,9 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
     for (int e = 0; e < E; ++e) {
       const int ch = ((e * W + part) * 64 + lane) * 8;
       if (ch < a.D) {
-        rg[e].load((const T*)a.dy + row * a.D + ch);
-        rh[e].load((const TR*)a.h + row * a.h_stride + ch);
-        if constexpr (DH) rd[e].load((const TR*)a.dh + row * a.D + ch);
+        load_stream(rg[e], (const T*)a.dy + row * a.D + ch);
+        load_stream(rh[e], (const TR*)a.h + row * a.h_stride + ch);
+        if constexpr (DH) load_stream(rd[e], (const TR*)a.dh + row * a.D + ch);
       } else {
         rg[e].zero();
         rh[e].zero();
@@ -277,19 +278,23 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
   }
 }
 
-// The weight's gradient: 8 channels a workgroup, 32 lanes each walking the partial sums.
-__global__ void __launch_bounds__(256) gdn2_residual_norm_dweight_kernel(const float* partial, float* dweight, int D, int groups) {
-  __shared__ float s[32][8];
-  const int c = threadIdx.x & 7, k = threadIdx.x >> 3;
+// The weight's gradient: 32 channels (a line of the partial sums) a workgroup, 32 of its lanes walking
+// the sums of each.
+__global__ void __launch_bounds__(1024) gdn2_residual_norm_dweight_kernel(const float* partial, float* dweight, int D, int groups) {
+  __shared__ float s[32][32];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5, ch = blockIdx.x * 32 + c;
   float x = 0.f;
-  for (int g = k; g < groups; g += 32) x += partial[(long)g * D + blockIdx.x * 8 + c];
+  if (ch < D) {
+#pragma unroll 16
+    for (int g = k; g < groups; g += 32) x += partial[(long)g * D + ch];
+  }
   s[k][c] = x;
   __syncthreads();
-  if (threadIdx.x < 8) {
+  if (k == 0 && ch < D) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
-    dweight[blockIdx.x * 8 + threadIdx.x] = t;
+    for (int i = 0; i < 32; ++i) t += s[i][c];
+    dweight[ch] = t;
   }
 }
 
@@ -341,7 +346,7 @@ hipError_t norm_bwd_launch(const ResidualNormBwdArgs& a) {
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(gdn2_residual_norm_dweight_kernel, dim3((unsigned)(a.D / 8)), dim3(256), 0, st, a.partial, a.dweight, a.D, groups);
+  hipLaunchKernelGGL(gdn2_residual_norm_dweight_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(1024), 0, st, a.partial, a.dweight, a.D, groups);
   return hipGetLastError();
 }
 

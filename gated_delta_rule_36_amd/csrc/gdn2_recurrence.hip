@@ -16,6 +16,7 @@
 // for thousands of tokens takes one rounding of its decay per run and not per token.
 
 #include "gdn2_attn_device.h"
+#include "gdn2_stack_device.h"
 #include "gdn2_stack_launch.h"
 
 namespace gdn2 {
@@ -65,24 +66,6 @@ __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
   p.begin = begin < p.len || p.index == 0 ? (int)begin : p.len + 1;
   p.end = begin + a.cut.seg < p.len ? (int)begin + a.cut.seg : p.len;
   return p;
-}
-
-template <typename T>
-__device__ __forceinline__ void store8_stream(T* p, const float* f) {
-  if constexpr (sizeof(T) == 2) {
-    bf16x8 v;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = static_cast<bf16>(f[i]);
-    __builtin_nontemporal_store(v, reinterpret_cast<bf16x8*>(p));
-  } else {
-    __builtin_nontemporal_store(f4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f4*>(p));
-    __builtin_nontemporal_store(f4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f4*>(p) + 1);
-  }
-}
-__device__ __forceinline__ void load8f(const float* p, float* f) {
-  const f4 x = reinterpret_cast<const f4*>(p)[0], y = reinterpret_cast<const f4*>(p)[1];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { f[i] = x[i]; f[4 + i] = y[i]; }
 }
 
 // x of the lower and of the upper half of every group of 2 STEP lanes, in all of its lanes at the
@@ -182,17 +165,6 @@ template <typename T, int R, int ARRAYS>
 struct Raw {
   Vec8<T> x[ARRAYS][R];
 };
-
-// Eight channels that are read once: past the caches' retention.
-__device__ __forceinline__ void load_stream(Vec8<bf16>& r, const bf16* p) {
-  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-  r.r = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)));
-}
-__device__ __forceinline__ void load_stream(Vec8<float>& r, const float* p) {
-  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-  r.r0 = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)));
-  r.r1 = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p) + 1));
-}
 
 }  // namespace
 
