@@ -26,16 +26,16 @@ def _code(dt):
 
 def _row_stride(name, t):
     """Elements from one row (of the last axis) to the next; rows dense and at one stride."""
+    if t.is_contiguous():
+        return t.shape[-1]
     D = t.shape[-1]
-    if t.is_contiguous() or t.numel() <= D:
-        if D > 1 and t.stride(-1) != 1 and t.numel():
-            raise ValueError(f"{name}: the channels must be dense, got strides {t.stride()}")
-        return D
     try:
         step, inner = t.view(-1, D).stride()
     except RuntimeError:
         step, inner = 0, 0
-    if inner != 1 or step < D or step % 8:
+    if t.numel() == D:
+        step = D  # one row: no step is taken
+    if (inner != 1 and D > 1) or step < D or step % 8:
         raise ValueError(f"{name}: rows must be dense and at one stride, a multiple of 8 elements, "
                          f"got strides {t.stride()} for shape {tuple(t.shape)}")
     return step
@@ -233,10 +233,11 @@ def _norm(x, residual, weight, eps, group, out):
     if group is not None:
         if group not in (0, 32, 64, 128) or (group and D % group):
             raise ValueError(f"group: 0 (a scale for every row), 32, 64 or 128 dividing {D} channels, got {group}")
-        scale = torch.empty(*shape[:-1], D // (group or D), dtype=torch.float32, device=dev)
+        scale = weight.new_empty(shape[:-1] + (D // (group or D),))
     if out is None:
-        y = torch.empty(shape, dtype=dt if group is None else torch.float8_e4m3fn, device=dev)
-        h = x if residual is None else torch.empty(shape, dtype=residual.dtype, device=dev)
+        kind = dt if group is None else torch.float8_e4m3fn
+        y = torch.empty_like(x, dtype=kind) if x.is_contiguous() else x.new_empty(shape, dtype=kind)
+        h = x if residual is None else _empty(residual)
     else:
         y, h = out
         _dense("out[0]", y, shape, dt if group is None else torch.float8_e4m3fn, dev)

@@ -6,8 +6,7 @@
 // u = dy weight and n = h rho:
 //     dh_total = dh + rho (u - n mean(u n)) = dx = dr,   dweight = sum over rows of dy n.
 //
-// Bound by HBM: every row is read once and kept in registers between the sum and the output. A row
-// belongs to one wave (no barrier) or, where rows are few or wide, to the 4 waves of a workgroup.
+// Bound by HBM: every row is read once and kept in registers between the sum and the output.
 
 #include <type_traits>
 
@@ -19,24 +18,33 @@ namespace gdn2 {
 
 namespace {
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T x) {
+// Sum over the LANES lanes of a row.
+template <int LANES, typename T>
+__device__ __forceinline__ T lanes_sum(T x) {
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
+  for (int m = LANES / 2; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
   return x;
 }
 
-// Sum over the W waves of a row: W = 4 through LDS (s: 4 values of this call's own).
-template <int W, typename T>
-__device__ __forceinline__ T row_total(T x, T* s, int wave) {
-  x = wave_sum(x);
+// Sums over a row of K values: LANES lanes of a wave, and W waves through LDS (s: of this call's own).
+template <int LANES, int W, int K, typename T>
+__device__ __forceinline__ void row_total(T (&x)[K], T (*s)[W], int wave) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = lanes_sum<LANES>(x[k]);
   if constexpr (W > 1) {
-    if ((threadIdx.x & 63) == 0) s[wave] = x;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[k][wave] = x[k];
+    }
     __syncthreads();
-    x = ((s[0] + s[1]) + (s[2] + s[3]));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      x[k] = 0;
+#pragma unroll
+      for (int u = 0; u < W; ++u) x[k] += s[k][u];
+    }
     __syncthreads();
   }
-  return x;
 }
 
 // 2^k with the smallest k in [-64, 126] for which amax <= 448 * 2^k; NaN and zero give 2^-64.
@@ -65,16 +73,17 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* f) {
 
 }  // namespace
 
-// E steps of 8 channels a lane; W waves a row. BITS8: the output in 8 bits. There the mean square
-// and the groups' maxima are formed in fp64 (h and weight are exact in it, so is their product):
-// the scale steps where a maximum passes 448 times a power of two, and must not step by a rounding.
-template <typename T, typename TR, int E, int W, bool ADD, bool BITS8>
-__global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArgs a) {
+// A row belongs to LANES lanes of a wave or (LANES = 64) to W waves, which hold E steps of 8 channels a
+// lane. BITS8: the output in 8 bits. There the mean square and the groups' maxima are formed in fp64
+// (h and weight are exact in it, so is their product): the scale steps where a maximum passes 448
+// times a power of two, and must not step by a rounding.
+template <typename T, typename TR, int LANES, int E, int W, bool ADD, bool BITS8>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_kernel(ResidualNormArgs a) {
   typedef typename std::conditional<BITS8, double, float>::type acc;
-  __shared__ acc s_sum[4];
-  const int lane = threadIdx.x & 63;
+  __shared__ acc s_sum[1][W];
+  const int lane = threadIdx.x & 63, in_row = lane % LANES;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long row = W == 1 ? (long)blockIdx.x * 4 + wave : (long)blockIdx.x;
+  const long row = W == 1 ? ((long)blockIdx.x * 4 + wave) * (64 / LANES) + lane / LANES : (long)blockIdx.x;
   if (W == 1 && row >= a.rows) return;
   const int part = W == 1 ? 0 : wave;
   const T* x = (const T*)a.x + row * a.x_stride;
@@ -83,17 +92,17 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
   Vec8<TR> rr[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int ch = ((e * W + part) * 64 + lane) * 8;
+    const int ch = ((e * W + part) * LANES + in_row) * 8;
     if (ch < a.D) {
       load_stream(rx[e], x + ch);
       if constexpr (ADD) load_stream(rr[e], r + ch);
     }
   }
   float h[E][8];
-  acc ss = 0;
+  acc sum[1] = {0};
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int ch = ((e * W + part) * 64 + lane) * 8;
+    const int ch = ((e * W + part) * LANES + in_row) * 8;
     if (ch < a.D) {
       rx[e].to_float(h[e]);
       if constexpr (ADD) {
@@ -108,14 +117,15 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
       for (int c = 0; c < 8; ++c) h[e][c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) ss += (acc)h[e][c] * (acc)h[e][c];
+    for (int c = 0; c < 8; ++c) sum[0] += (acc)h[e][c] * (acc)h[e][c];
   }
-  ss = row_total<W>(ss, s_sum, wave);
+  row_total<LANES, W>(sum, s_sum, wave);
+  const acc ss = sum[0];
   if constexpr (!BITS8) {
     const float rho = rsqrtf(ss / a.D + a.eps);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       if (ch < a.D) {
         const f4 w0 = reinterpret_cast<const f4*>(a.weight + ch)[0], w1 = reinterpret_cast<const f4*>(a.weight + ch)[1];
         float y[8];
@@ -127,12 +137,12 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
   } else {
     const double rho = 1.0 / sqrt(ss / a.D + (double)a.eps);
     const float rho32 = (float)rho;
-    const bool whole = a.group >= a.D;  // one scale a row (128 channels or fewer: the row itself)
-    const int lanes = whole ? 64 : a.group / 8;
+    const bool whole = a.group >= a.D;  // one scale a row
+    const int lanes = a.group / 8;  // of a group
     double big[E], most = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       big[e] = 0;
       if (ch < a.D) {
         const f4 w0 = reinterpret_cast<const f4*>(a.weight + ch)[0], w1 = reinterpret_cast<const f4*>(a.weight + ch)[1];
@@ -147,20 +157,20 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
       most = most > big[e] || most != most ? most : big[e];
     }
     if (whole) {
-      most = lanes_max(most, 64);
+      most = lanes_max(most, LANES);
       if constexpr (W > 1) {
-        if (lane == 0) s_sum[wave] = most;
+        if (lane == 0) s_sum[0][wave] = most;
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const double y = s_sum[u];
+        for (int u = 0; u < W; ++u) {
+          const double y = s_sum[0][u];
           most = most > y || most != most ? most : y;
         }
       }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       const float s = power_scale((whole ? most : lanes_max(big[e], lanes)) * rho);
       if (ch < a.D) {
         const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));  // 1 / s, exact
@@ -176,16 +186,18 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_kernel(ResidualNormArg
 
 // Gradients. A wave (or workgroup) walks rows and keeps its part of the weight's gradient in
 // registers; each workgroup leaves one partial sum, which the second kernel adds in a fixed order.
-template <typename T, typename TR, int E, int W, bool DH>
-__global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
-  __shared__ __attribute__((aligned(16))) float s_part[W == 1 ? 4 : 1][W == 1 ? E * 512 : 8];
-  const int lane = threadIdx.x & 63;
+template <typename T, typename TR, int LANES, int E, int W, bool DH>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
+  constexpr int ROWS = W == 1 ? 4 * (64 / LANES) : 1;  // of a workgroup at a time
+  __shared__ __attribute__((aligned(16))) float s_part[ROWS][W == 1 ? E * LANES * 8 : 4];
+  __shared__ float s_sum[2][W];
+  const int lane = threadIdx.x & 63, in_row = lane % LANES;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = W == 1 ? 0 : wave;
   float w[E][8], dw[E][8];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int ch = ((e * W + part) * 64 + lane) * 8;
+    const int ch = ((e * W + part) * LANES + in_row) * 8;
 #pragma unroll
     for (int c = 0; c < 8; ++c) w[e][c] = dw[e][c] = 0.f;
     if (ch < a.D) {
@@ -194,13 +206,13 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
       for (int c = 0; c < 8; ++c) w[e][c] = c < 4 ? w0[c] : w1[c - 4];
     }
   }
-  const long step = (long)gridDim.x * (W == 1 ? 4 : 1);
-  for (long row = W == 1 ? (long)blockIdx.x * 4 + wave : (long)blockIdx.x; row < a.rows; row += step) {
+  const int mine = W == 1 ? wave * (64 / LANES) + lane / LANES : 0;
+  for (long row = (long)blockIdx.x * ROWS + mine; row < a.rows; row += (long)gridDim.x * ROWS) {
     Vec8<T> rg[E];
     Vec8<TR> rh[E], rd[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       if (ch < a.D) {
         load_stream(rg[e], (const T*)a.dy + row * a.D + ch);
         load_stream(rh[e], (const TR*)a.h + row * a.h_stride + ch);
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
         rh[e].zero();
       }
     }
-    float ss = 0.f, uh = 0.f;
+    float sum[2] = {0.f, 0.f};  // h^2, u h
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float g[8], h[8];
@@ -218,30 +230,17 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
       rh[e].to_float(h);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        ss = fmaf(h[c], h[c], ss);
-        uh = fmaf(g[c] * w[e][c], h[c], uh);
+        sum[0] = fmaf(h[c], h[c], sum[0]);
+        sum[1] = fmaf(g[c] * w[e][c], h[c], sum[1]);
       }
     }
-    if constexpr (W == 1) {
-      ss = wave_sum(ss);
-      uh = wave_sum(uh);
-    } else {
-      ss = wave_sum(ss);
-      uh = wave_sum(uh);
-      if (lane == 0) {
-        s_part[0][wave] = ss;
-        s_part[0][4 + wave] = uh;
-      }
-      __syncthreads();
-      ss = (s_part[0][0] + s_part[0][1]) + (s_part[0][2] + s_part[0][3]);
-      uh = (s_part[0][4] + s_part[0][5]) + (s_part[0][6] + s_part[0][7]);
-      __syncthreads();
-    }
+    row_total<LANES, W>(sum, s_sum, wave);
+    const float ss = sum[0], uh = sum[1];
     const float rho = rsqrtf(ss / a.D + a.eps);
     const float back = rho * rho * (uh / a.D);  // rho mean(u n)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       if (ch < a.D) {
         float g[8], h[8], d[8];
         rg[e].to_float(g);
@@ -261,18 +260,18 @@ __global__ void __launch_bounds__(256) gdn2_residual_norm_bwd_kernel(ResidualNor
   float* const out = a.partial + (long)blockIdx.x * a.D;
   if constexpr (W == 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) store8(&s_part[wave][(e * 64 + lane) * 8], dw[e]);
+    for (int e = 0; e < E; ++e) store8(&s_part[mine][(e * LANES + in_row) * 8], dw[e]);
     __syncthreads();
     for (int ch = threadIdx.x * 4; ch < a.D; ch += 1024) {
       f4 s = *reinterpret_cast<const f4*>(&s_part[0][ch]);
 #pragma unroll
-      for (int u = 1; u < 4; ++u) s += *reinterpret_cast<const f4*>(&s_part[u][ch]);
+      for (int u = 1; u < ROWS; ++u) s += *reinterpret_cast<const f4*>(&s_part[u][ch]);
       *reinterpret_cast<f4*>(out + ch) = s;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = ((e * W + part) * 64 + lane) * 8;
+      const int ch = ((e * W + part) * LANES + in_row) * 8;
       if (ch < a.D) store8(out + ch, dw[e]);
     }
   }
@@ -300,49 +299,54 @@ __global__ void __launch_bounds__(1024) gdn2_residual_norm_dweight_kernel(const 
 
 namespace {
 
-// Waves of a row: one up to 2048 channels, unless rows are too few to fill the card.
-int waves_of(long rows, int D) { return D > 2048 || rows < 1024 ? 4 : 1; }
-
-// Calls f(E) with the steps of a lane for D channels and W waves.
+// How a row is laid out. Up to 512 channels it takes no more lanes of a wave than it fills (65536 rows
+// of 256: 30 -> 26 us, backward 43 -> 28); wider ones take a wave up to 2048 channels, unless rows are too few to fill the
+// card, and 4 or 8 waves above.
+template <int LANES_, int E_, int W_>
+struct Layout {
+  static constexpr int LANES = LANES_, E = E_, W = W_;
+  static constexpr int rows = W == 1 ? 4 * (64 / LANES) : 1;  // of a workgroup
+  static constexpr int threads = W == 1 ? 256 : 64 * W;
+};
 template <typename F>
-hipError_t with_steps(int D, int W, F f) {
-  const int e = (D + W * 512 - 1) / (W * 512);
-  if (e <= 1) return f(std::integral_constant<int, 1>());
-  if (e <= 2) return f(std::integral_constant<int, 2>());
-  if (e <= 4) return f(std::integral_constant<int, 4>());
-  return f(std::integral_constant<int, 8>());
+auto with_layout(long rows, int D, F f) {
+  if (D <= 64) return f(Layout<8, 1, 1>());
+  if (D <= 128) return f(Layout<16, 1, 1>());
+  if (D <= 256) return f(Layout<32, 1, 1>());
+  if (D <= 512) return f(Layout<64, 1, 1>());
+  if (D <= 2048 && rows >= 1024) return D <= 1024 ? f(Layout<64, 2, 1>()) : f(Layout<64, 4, 1>());
+  if (D <= 2048) return f(Layout<64, 1, 4>());
+  if (D <= 4096) return f(Layout<64, 2, 4>());
+  if (D <= 8192) return f(Layout<64, 4, 4>());
+  return f(Layout<64, 4, 8>());
 }
 
-template <typename T, typename TR, int W>
+template <typename T, typename TR>
 hipError_t norm_launch(const ResidualNormArgs& a) {
-  return with_steps(a.D, W, [&](auto steps) {
-    constexpr int E = decltype(steps)::value;
-    const dim3 grid((unsigned)(W == 1 ? (a.rows + 3) / 4 : a.rows)), block(256);
+  return with_layout(a.rows, a.D, [&](auto layout) {
+    typedef decltype(layout) L;
+    const dim3 grid((unsigned)((a.rows + L::rows - 1) / L::rows)), block(L::threads);
     const hipStream_t st = (hipStream_t)a.stream;
-    if constexpr (W == 4 || E <= 4) {
-      if (a.scale) {
-        if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, true, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, false, true>), grid, block, 0, st, a);
-      } else {
-        if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, true, false>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, E, W, false, false>), grid, block, 0, st, a);
-      }
+    if (a.scale) {
+      if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, L::LANES, L::E, L::W, true, true>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, T, L::LANES, L::E, L::W, false, true>), grid, block, 0, st, a);
+    } else {
+      if (a.r) hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, TR, L::LANES, L::E, L::W, true, false>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((gdn2_residual_norm_kernel<T, T, L::LANES, L::E, L::W, false, false>), grid, block, 0, st, a);
     }
     return hipGetLastError();
   });
 }
 
-template <typename T, typename TR, int W>
+template <typename T, typename TR>
 hipError_t norm_bwd_launch(const ResidualNormBwdArgs& a) {
   const int groups = residual_norm_bwd_groups(a.rows, a.D);
   const hipStream_t st = (hipStream_t)a.stream;
-  const hipError_t err = with_steps(a.D, W, [&](auto steps) {
-    constexpr int E = decltype(steps)::value;
-    const dim3 grid((unsigned)groups), block(256);
-    if constexpr (W == 4 || E <= 4) {
-      if (a.dh) hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, E, W, true>), grid, block, 0, st, a);
-      else hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, E, W, false>), grid, block, 0, st, a);
-    }
+  const hipError_t err = with_layout(a.rows, a.D, [&](auto layout) {
+    typedef decltype(layout) L;
+    const dim3 grid((unsigned)groups), block(L::threads);
+    if (a.dh) hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, L::LANES, L::E, L::W, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((gdn2_residual_norm_bwd_kernel<T, TR, L::LANES, L::E, L::W, false>), grid, block, 0, st, a);
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
@@ -353,22 +357,18 @@ hipError_t norm_bwd_launch(const ResidualNormBwdArgs& a) {
 }  // namespace
 
 int residual_norm_bwd_groups(long rows, int D) {
-  const long full = waves_of(rows, D) == 1 ? (rows + 3) / 4 : rows;
+  const long full = with_layout(rows, D, [&](auto layout) { return (rows + decltype(layout)::rows - 1) / decltype(layout)::rows; });
   return (int)(full < 512 ? full : 512);
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a) {
-  const bool one = waves_of(a.rows, a.D) == 1;
-  if (a.dtype == 1) return one ? norm_launch<float, float, 1>(a) : norm_launch<float, float, 4>(a);
-  if (a.r_dtype == 1) return one ? norm_launch<bf16, float, 1>(a) : norm_launch<bf16, float, 4>(a);
-  return one ? norm_launch<bf16, bf16, 1>(a) : norm_launch<bf16, bf16, 4>(a);
+  if (a.dtype == 1) return norm_launch<float, float>(a);
+  return a.r_dtype == 1 ? norm_launch<bf16, float>(a) : norm_launch<bf16, bf16>(a);
 }
 
 hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a) {
-  const bool one = waves_of(a.rows, a.D) == 1;
-  if (a.dtype == 1) return one ? norm_bwd_launch<float, float, 1>(a) : norm_bwd_launch<float, float, 4>(a);
-  if (a.r_dtype == 1) return one ? norm_bwd_launch<bf16, float, 1>(a) : norm_bwd_launch<bf16, float, 4>(a);
-  return one ? norm_bwd_launch<bf16, bf16, 1>(a) : norm_bwd_launch<bf16, bf16, 4>(a);
+  if (a.dtype == 1) return norm_bwd_launch<float, float>(a);
+  return a.r_dtype == 1 ? norm_bwd_launch<bf16, float>(a) : norm_bwd_launch<bf16, bf16>(a);
 }
 
 }  // namespace gdn2

@@ -45,6 +45,9 @@ CASES = [
     (2, 16384, "bf16", "fp32", False), (1027, 64, "bf16", "bf16", True), (1025, 512, "fp32", "fp32", False),
     (1030, 520, "bf16", "fp32", False), (1024, 1032, "bf16", "bf16", False), (1029, 2048, "bf16", "fp32", True),
     (1031, 2040, "fp32", None, False),
+    # several rows a wave
+    (37, 56, "bf16", "bf16", True), (29, 128, "fp32", "fp32", False), (31, 104, "bf16", "fp32", True),
+    (9, 256, "bf16", "fp32", False), (2050, 136, "bf16", None, True), (3, 512, "bf16", "bf16", False),
 ]
 
 
@@ -84,7 +87,7 @@ def test_backward(case):
 def test_backward_many_rows():
     """More rows than the backward's waves: each then walks several."""
     import gated_delta_rule_36_amd as G
-    for rows, D, rt in ((5000, 72, "bf16"), (1100, 2056, "fp32")):
+    for rows, D, rt in ((20000, 24, "bf16"), (9000, 128, "fp32"), (5000, 200, "bf16"), (2500, 520, "bf16"), (1100, 2056, "fp32"), (600, 9000, "bf16")):
         x, r, w, rng = _case(3, rows, D, "bf16", rt)
         h, dy = _stream(x, r).cuda(), draw(rng, rows, D).cuda()
         say("residual_norm_bwd", rows, D)
@@ -97,7 +100,7 @@ def test_backward_many_rows():
 
 
 GROUPS = [(1, 32, 32), (5, 96, 32), (3, 64, 0), (7, 1000, 0), (2, 2048, 64), (4, 2048, 0), (3, 4096, 128), (2, 4224, 32),
-          (1, 8192, 0), (1, 16384, 64), (2, 128, 128), (1030, 512, 32), (1026, 1024, 0), (1025, 1920, 128), (1024, 520, 0)]
+          (1, 8192, 0), (1, 16384, 64), (2, 128, 128), (67, 64, 64), (70, 64, 0), (41, 128, 32), (18, 256, 0), (33, 256, 128), (1030, 512, 32), (1026, 1024, 0), (1025, 1920, 128), (1024, 520, 0)]
 
 
 @pytest.mark.parametrize("dt,rt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32"), ("bf16", None)])

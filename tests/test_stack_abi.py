@@ -103,8 +103,10 @@ def test_norm_refusals(bwd):
            (1, dict(D=0)), (2, dict(D=60)), (2, dict(D=16392, xs=16392, rs=16392, hs=16392)), (1, dict(eps=-1.0)),
            (1, dict(eps=math.nan)), (1, dict(eps=math.inf)), (1, dict(w=None)), (1, dict(w=M4)), (1, dict(h=None)), (1, dict(h=M4))]
     if bwd:
-        need = _lib.lib().gdn2_residual_norm_bwd_workspace_bytes(4, 64)
-        assert need == 4 * 64 * 4
+        ask = _lib.lib().gdn2_residual_norm_bwd_workspace_bytes
+        need = ask(4, 64)
+        assert need == 64 * 4 and ask(33, 64) == 2 * need          # 32 rows a workgroup
+        assert ask(7, 1000) == 7 * 1000 * 4 and ask(100000, 2048) == 512 * 2048 * 4
         assert _lib.lib().gdn2_residual_norm_bwd_workspace_bytes(4, 60) == 0
         assert _lib.lib().gdn2_residual_norm_bwd_workspace_bytes(0, 64) == 0
         bad += [(1, dict(hs=60)), (1, dict(dy=None)), (1, dict(dx=None)), (1, dict(dw=None)), (1, dict(dh=M4)), (1, dict(dr=F)),
