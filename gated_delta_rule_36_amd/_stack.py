@@ -83,7 +83,8 @@ def _recurrence_sizes(backward, packed, B, T, D, N):
 
 
 def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
-    B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
+    sizes = _recurrence_args(v, g, w, cu_seqlens)
+    B, T, D, N, strides, code, dev, dt = sizes
     if initial_state is not None:
         _dense("initial_state", initial_state, (N, D), torch.float32, dev)
     o = _empty(v)
@@ -93,7 +94,7 @@ def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
     ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence", dev, v.data_ptr(), g.data_ptr(), _p(w), _p(initial_state),
           o.data_ptr(), _p(last), _p(states), _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
-    return o, last, states
+    return o, last, states, sizes
 
 
 def linear_recurrence_fwd(v, g, w=None, initial_state=None, cu_seqlens=None,
@@ -113,7 +114,7 @@ def linear_recurrence_fwd_train(v, g, w=None, initial_state=None, cu_seqlens=Non
                                 output_final_state=True):
     """linear_recurrence_fwd for training: (o, final_state, states), the last for
     linear_recurrence_bwd (the fp32 state before every 64th token of every sequence)."""
-    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)
+    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)[:3]
 
 
 def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=None):
@@ -122,16 +123,24 @@ def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=No
 
     states: from linear_recurrence_fwd_train on the same inputs. do: [B, T, D] contiguous;
     d_final_state: fp32 [N, D] or None. Rows that belong to no packed sequence get zeros."""
-    B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
+    sizes = _recurrence_args(v, g, w, cu_seqlens)
+    B, T, D, N, strides, code, dev, dt = sizes
     _dense("do", do, (B, T, D), dt, dev)
-    need, slots = _recurrence_sizes(True, cu_seqlens is not None, B, T, D, N)
+    slots = _recurrence_sizes(True, cu_seqlens is not None, B, T, D, N)[1]
     _dense("states", states, (slots, D), torch.float32, dev)
     if d_final_state is not None:
         _dense("d_final_state", d_final_state, (N, D), torch.float32, dev)
+    return _recurrence_bwd(v, g, w, states, do, d_final_state, cu_seqlens, sizes)
+
+
+def _recurrence_bwd(v, g, w, states, do, d_final_state, cu_seqlens, sizes):
+    """The call itself, of checked tensors (autograd's are the forward's own)."""
+    B, T, D, N, strides, code, dev, dt = sizes
+    need = _recurrence_sizes(True, cu_seqlens is not None, B, T, D, N)[0]
     dv, dg = torch.empty_like(do), torch.empty_like(do)
     dw = None if w is None else torch.empty_like(do)
-    ds0 = torch.empty((N, D), dtype=torch.float32, device=dev)
-    ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
+    ds0 = states.new_empty((N, D))
+    ws = states.new_empty(need // 4) if need else None
     _call("gdn2_linear_recurrence_bwd", dev, v.data_ptr(), g.data_ptr(), _p(w), states.data_ptr(),
           do.data_ptr(), _p(d_final_state), dv.data_ptr(), dg.data_ptr(), _p(dw), ds0.data_ptr(),
           _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
@@ -141,7 +150,7 @@ def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=No
 class _LinearRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, v, g, w, initial_state, cu_seqlens):
-        o, last, states = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
+        o, last, states, ctx.sizes = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
         ctx.set_materialize_grads(False)
         ctx.has_s0 = initial_state is not None
         ctx.save_for_backward(v, g, w, states, cu_seqlens)
@@ -153,7 +162,7 @@ class _LinearRecurrence(torch.autograd.Function):
         v, g, w, states, cu = ctx.saved_tensors
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _aligned_gradient(do)
         d_last = None if d_last is None else _aligned_gradient(d_last)
-        dv, dg, dw, ds0 = linear_recurrence_bwd(v, g, w, states, do, d_last, cu)
+        dv, dg, dw, ds0 = _recurrence_bwd(v, g, w, states, do, d_last, cu, ctx.sizes)
         return dv, dg, dw, ds0 if ctx.has_s0 else None, None
 
 
@@ -289,21 +298,27 @@ def residual_norm_bwd(dy, dh, h, weight, eps=1e-6):
     """Gradients of residual_norm_fwd for the gradients dy (contiguous, x's type) and dh (contiguous,
     h's type; None: zero) of its outputs, from h as it returned it: (dx, dresidual, dweight). dx and
     dresidual are the same values (one tensor where the types agree), dweight is fp32 [D]."""
-    shape, D, rows, hs, _, hcode, _, dev, ht = _norm_args(h, None, weight)
-    code = _code(dy.dtype)
-    if code > hcode:
+    shape, _, _, _, _, hcode, _, dev, ht = _norm_args(h, None, weight)
+    if _code(dy.dtype) > hcode:
         raise TypeError(f"dy: {dy.dtype} is wider than h's {ht}")
     _dense("dy", dy, shape, dy.dtype, dev)
     if dh is not None:
         _dense("dh", dh, shape, ht, dev)
+    return _norm_bwd(dy, dh, h, weight, eps)
+
+
+def _norm_bwd(dy, dh, h, weight, eps):
+    """The call itself, of checked tensors (autograd's are the forward's own)."""
+    D = weight.numel()
+    rows, code, hcode = dy.numel() // D, _CODES[dy.dtype], _CODES[h.dtype]
     dx = torch.empty_like(dy)
-    dr = dx if code == hcode else torch.empty(shape, dtype=ht, device=dev)
+    dr = dx if code == hcode else torch.empty_like(dy, dtype=h.dtype)
     dw = torch.empty_like(weight) if rows else torch.zeros_like(weight)
     need = _norm_workspace(rows, D)
     ws = weight.new_empty(need // 4)
-    _call("gdn2_residual_norm_bwd", dev, dy.data_ptr(), _p(dh), h.data_ptr(), weight.data_ptr(),
-          dx.data_ptr(), None if code == hcode else dr.data_ptr(), dw.data_ptr(), rows, D, hs, eps,
-          code, hcode, ws.data_ptr(), need)
+    _call("gdn2_residual_norm_bwd", dy.device, dy.data_ptr(), _p(dh), h.data_ptr(),
+          weight.data_ptr(), dx.data_ptr(), None if code == hcode else dr.data_ptr(),
+          dw.data_ptr(), rows, D, _row_stride("h", h), eps, code, hcode, ws.data_ptr(), need)
     return dx, dr, dw
 
 
@@ -323,7 +338,7 @@ class _ResidualNorm(torch.autograd.Function):
         h, weight = ctx.saved_tensors
         dy = torch.zeros(h.shape, dtype=ctx.dt, device=h.device) if dy is None else _aligned_gradient(dy)
         dh = None if dh is None else _aligned_gradient(dh)
-        dx, dr, dw = residual_norm_bwd(dy, dh, h, weight, ctx.eps)
+        dx, dr, dw = _norm_bwd(dy, dh, h, weight, ctx.eps)
         return dx, dr if ctx.needs_input_grad[1] else None, dw, None
 
 

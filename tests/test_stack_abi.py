@@ -277,18 +277,18 @@ def test_gradients_at_any_offset(monkeypatch, shift):
     held = {}
     monkeypatch.setattr(_stack, "_need_gpu", lambda t: None)
     monkeypatch.setattr(_stack, "_call", lambda *a: None)
-    real = {n: getattr(_stack, n) for n in ("linear_recurrence_bwd", "residual_norm_bwd")}
+    real = {n: getattr(_stack, n) for n in ("_recurrence_bwd", "_norm_bwd")}
 
-    def rec(v, g, w, states, do, d_last, cu):
+    def rec(v, g, w, states, do, d_last, *rest):
         held.update(a=do, b=d_last)
-        return real["linear_recurrence_bwd"](v, g, w, states, do, d_last, cu)
+        return real["_recurrence_bwd"](v, g, w, states, do, d_last, *rest)
 
     def norm(dy, dh, h, w, eps):
         held.update(a=dy, b=dh)
-        return real["residual_norm_bwd"](dy, dh, h, w, eps)
+        return real["_norm_bwd"](dy, dh, h, w, eps)
 
-    monkeypatch.setattr(_stack, "linear_recurrence_bwd", rec)
-    monkeypatch.setattr(_stack, "residual_norm_bwd", norm)
+    monkeypatch.setattr(_stack, "_recurrence_bwd", rec)
+    monkeypatch.setattr(_stack, "_norm_bwd", norm)
     x = torch.zeros(1, 3, 64, requires_grad=True)
     for pair in (G.linear_recurrence(x, x), G.residual_norm(x, x * 1, torch.ones(64))):
         flat = torch.cat([torch.zeros(shift), pair[0].flatten(), pair[1].flatten()])
