@@ -113,7 +113,8 @@ def linear_recurrence_fwd(v, g, w=None, initial_state=None, cu_seqlens=None,
 def linear_recurrence_fwd_train(v, g, w=None, initial_state=None, cu_seqlens=None,
                                 output_final_state=True):
     """linear_recurrence_fwd for training: (o, final_state, states), the last for
-    linear_recurrence_bwd (the fp32 state before every 64th token of every sequence)."""
+    linear_recurrence_bwd (the fp32 state before every 64th token of every sequence). Rows that belong
+    to no packed sequence are zeros."""
     return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)[:3]
 
 
@@ -168,7 +169,8 @@ class _LinearRecurrence(torch.autograd.Function):
 
 def linear_recurrence(v, g, w=None, initial_state=None, cu_seqlens=None):
     """Differentiable linear_recurrence_fwd: (o, final_state); gradients flow to v, g, w and the
-    initial state through the library's backward. (torch ties a leaf's accumulation to the stream of
+    initial state through the library's backward. Rows that belong to no packed sequence are zeros, and
+    so are their gradients. (torch ties a leaf's accumulation to the stream of
     its first use: before a backward pass is captured into a graph, drop eager results of the same
     leaves that are still alive.)"""
     return _LinearRecurrence.apply(v, g, w, initial_state, cu_seqlens)

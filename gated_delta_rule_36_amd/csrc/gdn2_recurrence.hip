@@ -37,11 +37,12 @@ struct Piece {
   int index;       // which segment (0 .. ), and in all the sequence's
   int begin, end;  // its tokens
 };
-// Unit u: segment u % per_sequence of sequence u / per_sequence; packed, sequence n's units begin at
-// cu_seqlens[n] / seg + n. A unit past its sequence's end has begin > end (begin = end = 0 stands for
-// a sequence without tokens).
+// Unit u: segment u % per_sequence of sequence u / per_sequence; packed and cut, sequence n's units
+// begin at cu_seqlens[n] / seg + n. A unit that no segment has (in front of the first sequence's, past
+// a sequence's end) has begin > end; a sequence without tokens has begin = end = 0.
 __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
   Piece p;
+  bool none = false;
   if (a.cu_seqlens == nullptr) {
     p.n = u / a.cut.per_sequence;
     p.index = u % a.cut.per_sequence;
@@ -54,8 +55,9 @@ __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
     if (a.cut.cut) {
       auto unit = [&](int i) { return (long)(clamped_offset(a.cu_seqlens, i, a.T) / a.cut.seg + i); };
       p.n = wave_search(a.N, u, unit);
-      p.index = __builtin_amdgcn_readfirstlane(u - (int)unit(p.n));
-      if (p.index < 0) p.index = 0;
+      p.index = uniform(u - (int)unit(p.n));
+      none = p.index < 0;
+      if (none) p.index = 0;
     }
     const int b = uniform(clamped_offset(a.cu_seqlens, p.n, a.T)), e = uniform(clamped_offset(a.cu_seqlens, p.n + 1, a.T));
     p.first = b;
@@ -63,7 +65,8 @@ __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
     p.slot = b / kStateTokens + p.n;
   }
   const long begin = (long)p.index * a.cut.seg;
-  p.begin = begin < p.len || p.index == 0 ? (int)begin : p.len + 1;
+  none = none || (p.index > 0 && begin >= p.len);
+  p.begin = none ? p.len + 1 : (int)begin;
   p.end = begin + a.cut.seg < p.len ? (int)begin + a.cut.seg : p.len;
   return p;
 }
@@ -189,7 +192,17 @@ struct Rows {
   }
 };
 
-// One workgroup a (unit, 64 channels). A tile's registers are filled with the next tile's inputs as
+// Zeros in the rows of a packed batch that belong to no sequence, 64 channels a workgroup.
+template <typename T>
+__device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, int ch, bool live) {
+  const int first = clamped_offset(a.cu_seqlens, 0, a.T), last = clamped_offset(a.cu_seqlens, a.N, a.T);
+  const float zero[8] = {};
+  for (int t = threadIdx.x >> 3; t < a.T; t += blockDim.x >> 3)
+    if (live && (t < first || t >= last)) store8(x + (long)t * a.D + ch, zero);
+}
+
+// One workgroup a (unit, 64 channels), and where states are kept for the backward of a packed batch one
+// row of them more, for the rows of no sequence. A tile's registers are filled with the next tile's inputs as
 // soon as its values are widened to fp32, so that loads are in flight during the scan and the stores.
 template <typename T, bool GATE, int NW>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs a) {
@@ -200,11 +213,15 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
-  const Piece p = piece_of(a, unit);
-  if (p.begin > p.end) return;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
   const int ch = strip + cg * 8;
   const bool live = ch < a.D;
+  if (unit == a.cut.units) {
+    zero_outside(a, (T*)a.o, ch, live);
+    return;
+  }
+  const Piece p = piece_of(a, unit);
+  if (p.begin > p.end) return;
   const int chl = live ? ch : a.D - 8;  // lanes past the channels load some of the last ones
   // the channel whose state this lane carries from tile to tile
   const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
@@ -394,14 +411,9 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
   const int chl = live ? ch : a.D - 8;
   const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
   if (unit == a.cut.units) {
-    const int first = clamped_offset(a.cu_seqlens, 0, a.T), last = clamped_offset(a.cu_seqlens, a.N, a.T);
-    const float zero[8] = {};
-    for (int t = run; t < a.T; t += NW * 8)
-      if (live && (t < first || t >= last)) {
-        store8((T*)b.dv + (long)t * a.D + ch, zero);
-        store8((T*)b.dg + (long)t * a.D + ch, zero);
-        if (GATE) store8((T*)b.dw + (long)t * a.D + ch, zero);
-      }
+    zero_outside(a, (T*)b.dv, ch, live);
+    zero_outside(a, (T*)b.dg, ch, live);
+    if (GATE) zero_outside(a, (T*)b.dw, ch, live);
     return;
   }
   const Piece p = piece_of(a, unit);
@@ -606,7 +618,7 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
   c.seg = T > 0 ? T : 1;
   c.per_sequence = 1;
   c.units = N;
-  if (T < (backward ? 3 : 6) * TILE || N == 0) return c;
+  if (T < (backward ? 3 : 6) * TILE || N == 0 || N > kMaxGroups) return c;
   long seg = ((tokens * strips + 1023) / 1024 + TILE - 1) / TILE * TILE;  // the fair share
   if (seg < 2 * TILE) seg = 2 * TILE;
   const long rounds = (groups + 255) / 256;
@@ -618,7 +630,7 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
   c.cut = true;
   c.seg = (int)seg;
   c.per_sequence = packed ? 1 : (int)((T + seg - 1) / seg);
-  c.units = packed ? (int)(T / seg + N) : N * c.per_sequence;
+  c.units = packed ? (int)(T / seg) + N : N * c.per_sequence;
   return c;
 }
 long recurrence_groups(const RecurrenceCut& c, int D) { return ((long)c.units + 1) * strips_of(D); }
@@ -637,8 +649,9 @@ template <typename T, bool GATE>
 hipError_t forward(const RecurrenceArgs& a) {
   const hipStream_t st = (hipStream_t)a.stream;
   const int strips = strips_of(a.D);
-  const dim3 grid((unsigned)(a.cut.units * strips));
-  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), grid, dim3(256), 0, st, a, (const T*)nullptr);
+  const bool rest = a.cu_seqlens != nullptr && a.states != nullptr && a.o != nullptr;  // rows of no sequence
+  const dim3 grid((unsigned)((a.cut.units + rest) * strips));
+  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3((unsigned)(a.cut.units * strips)), dim3(256), 0, st, a, (const T*)nullptr);
   if (wide_groups(a.cut, strips)) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8>), grid, dim3(512), 0, st, a);
   else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4>), grid, dim3(256), 0, st, a);
   return hipGetLastError();

@@ -39,7 +39,7 @@ int check_recurrence(bool backward, const void* v, const void* g, const void* w,
       (w != nullptr && !token_stride_ok(w_stride, D)))
     return GDN2_INVALID_ARGUMENT;
   if ((long)B * T > (long)INT_MAX - 4096) return GDN2_INVALID_ARGUMENT;
-  if (gdn2::recurrence_groups(gdn2::recurrence_cut(backward, cu_seqlens != nullptr, B, T, D, N), D) > (long)INT_MAX)
+  if (gdn2::recurrence_groups(gdn2::recurrence_cut(backward, cu_seqlens != nullptr, B, T, D, N), D) > gdn2::kMaxGroups)
     return GDN2_INVALID_ARGUMENT;
   if ((long)B * T > 0 && (!v || !g)) return GDN2_INVALID_ARGUMENT;
   if (!all_aligned16({v, g, w}) || !aligned(cu_seqlens, 4)) return GDN2_INVALID_ARGUMENT;
@@ -65,7 +65,7 @@ int check_norm(int64_t rows, int D, float eps, int dtype, int r_dtype) {
   if (!(eps >= 0.f) || !std::isfinite(eps)) return GDN2_INVALID_ARGUMENT;
   if (D % 8 != 0 || D > gdn2::kNormMaxWidth) return GDN2_UNSUPPORTED;
   if (dtype == GDN2_F32 && r_dtype != GDN2_F32) return GDN2_UNSUPPORTED;
-  if (rows > (int64_t)INT_MAX) return GDN2_INVALID_ARGUMENT;
+  if (rows > gdn2::kMaxGroups) return GDN2_INVALID_ARGUMENT;
   return GDN2_OK;
 }
 
@@ -95,7 +95,8 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
   if (st != GDN2_OK) return st;
   if ((long)B * T > 0 && !o && !states) return GDN2_INVALID_ARGUMENT;
   if (!all_aligned16({initial_state, o, final_state, states, workspace})) return GDN2_INVALID_ARGUMENT;
-  if (N == 0) return GDN2_OK;
+  // (the training forward writes the rows of no sequence)
+  if (N == 0 && !(cu_seqlens && T > 0 && states && o)) return GDN2_OK;
   const size_t need = gdn2_linear_recurrence_workspace_bytes(0, cu_seqlens != nullptr, B, T, D, N);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN2_WORKSPACE_TOO_SMALL;
   gdn2::RecurrenceArgs a = recurrence_args(false, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride,
@@ -179,7 +180,7 @@ int gdn2_residual_norm(const void* x, const void* residual, const float* weight,
 }
 
 size_t gdn2_residual_norm_bwd_workspace_bytes(int64_t rows, int D) {
-  if (rows <= 0 || D <= 0 || D % 8 != 0 || D > gdn2::kNormMaxWidth || rows > (int64_t)INT_MAX) return 0;
+  if (rows <= 0 || D <= 0 || D % 8 != 0 || D > gdn2::kNormMaxWidth || rows > gdn2::kMaxGroups) return 0;
   return (size_t)gdn2::residual_norm_bwd_groups(rows, D) * D * sizeof(float);
 }
 
@@ -222,7 +223,7 @@ int gdn2_verify_drafts(const void* target_probs, const void* draft_probs, const 
       !aligned(draft_len, 4) || !aligned(uniforms, 4) || !aligned(tokens, 4) ||
       !aligned(commit_len, 4) || !aligned(workspace, 16))
     return GDN2_INVALID_ARGUMENT;
-  if ((long)N * gdn2::verify_pieces(V) > (long)INT_MAX) return GDN2_INVALID_ARGUMENT;
+  if ((long)N * gdn2::verify_pieces(V) > gdn2::kMaxGroups) return GDN2_INVALID_ARGUMENT;
   if (workspace == nullptr || workspace_bytes < gdn2_verify_drafts_workspace_bytes(N, V))
     return GDN2_WORKSPACE_TOO_SMALL;
   gdn2::VerifyArgs a{};

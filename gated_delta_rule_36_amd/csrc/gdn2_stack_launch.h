@@ -9,6 +9,8 @@
 
 namespace gdn2 {
 
+constexpr long kMaxGroups = (1L << 23) - 1;  // of a launch: 512 threads each stay below 2^32
+
 // ---- diagonal recurrence: h = exp(g) h + w v, a state per channel
 
 // How sequences are cut: into units of seg tokens.

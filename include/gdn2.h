@@ -523,13 +523,15 @@ size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, in
  *   final_state     : [N, D] fp32, or NULL; may be initial_state
  *   states          : NULL, or gdn2_linear_recurrence_states_bytes(...) bytes: the states before
  *                     every 64th token, which the backward reads
- *   cu_seqlens      : as for gdn2_chunk_fwd. Rows in front of the first packed sequence and behind
- *                     the last are not written.
+ *   cu_seqlens      : as for gdn2_chunk_fwd, but that rows in front of the first sequence and behind the
+ *                     last are allowed. They are not written.
  *   workspace       : at least gdn2_linear_recurrence_workspace_bytes(...) bytes (0: may be NULL),
  *                     16-byte aligned, free for the call's duration on `hip_stream`; calls that can
  *                     overlap, captured ones among them, need one each. Long sequences of few
  *                     channels are cut into segments that run in parallel.
- *   Supported: D a multiple of 8, both dtypes, B * T below 2^31 - 4096. A NaN or an infinity stays in its own sequence and
+ *   (With `states`, for training, rows that belong to no packed sequence are written as zeros.)
+ *   Supported: D a multiple of 8, both dtypes, B * T below 2^31 - 4096, N * D / 64 below 2^23 (D
+ *   rounded up to 64). A NaN or an infinity stays in its own sequence and
  *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 is a no-op.
  * Returns GDN2_OK or an error status.
  */
@@ -582,7 +584,7 @@ int gdn2_linear_recurrence_tokens(const void* v, const void* log_alpha, const vo
  *              its group. A row with a NaN or an infinity gives NaN codes where y is NaN.
  *   group    : 0, 32, 64 or 128 channels (0 without scale); D a multiple of it
  *   Supported: D a multiple of 8 up to 16384; types bf16 with bf16, bf16 with an fp32 residual, fp32
- *   with fp32. Magnitudes below 2^63, past which the mean square leaves fp32. rows = 0 is a no-op.
+ *   with fp32; rows below 2^23. Magnitudes below 2^63, past which the mean square leaves fp32. rows = 0 is a no-op.
  * Returns GDN2_OK or an error status.
  */
 int gdn2_residual_norm(const void* x, const void* residual, const float* weight, void* y, void* h,
@@ -626,7 +628,8 @@ size_t gdn2_residual_norm_bwd_workspace_bytes(int64_t rows, int D);
  *                  gdn2_decode_tokens and gdn2_linear_recurrence_tokens.
  *   workspace    : at least gdn2_verify_drafts_workspace_bytes(N, V) bytes, 16-byte aligned; calls
  *                  that can overlap need one each
- *   N = 0 is a no-op. Returns GDN2_OK or an error status.
+ *   N * V / 4096 below 2^23 (V rounded up to 4096). N = 0 is a no-op. Returns GDN2_OK or an error
+ *   status.
  */
 int gdn2_verify_drafts(const void* target_probs, const void* draft_probs, const int32_t* drafts,
                        const int32_t* draft_len, const float* uniforms, int32_t* tokens,

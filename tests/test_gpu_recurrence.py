@@ -19,13 +19,14 @@ def _need_gpu():
         pytest.skip("no GPU")
 
 
-def _case(seed, B, T, D, dt, gate=True, start=True, lens=None, strided=False, decay=0.3, tail=0):
-    """Inputs on the device and in float64. lens: a packed batch; tail: rows behind its last sequence."""
+def _case(seed, B, T, D, dt, gate=True, start=True, lens=None, strided=False, decay=0.3, tail=0, front=0):
+    """Inputs on the device. lens: a packed batch; tail, front: rows behind its last sequence and in front
+    of its first."""
     rng = np.random.default_rng(seed)
     dtype = DT[dt]
     cu = None
     if lens is not None:
-        B, T, cu = 1, int(sum(lens)) + tail, np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        B, T, cu = 1, front + int(sum(lens)) + tail, (front + np.concatenate([[0], np.cumsum(lens)])).astype(np.int32)
     x = draw(rng, B, T, 3 * D + 8, dtype=torch.float32)
     x[..., D:2 * D] = -decay * torch.nn.functional.softplus(x[..., D:2 * D])
     x[..., 2 * D:3 * D] = torch.sigmoid(x[..., 2 * D:3 * D])
@@ -113,6 +114,46 @@ def test_backward(case):
         assert_within(name, x, r, bound)
     if tail:
         assert not got[0][:, end:].any() and not got[1][:, end:].any()
+
+
+@pytest.mark.parametrize("lens,front,tail", [([40, 0, 70], 30, 20), ([1500, 0, 700], 600, 300), ([900], 5000, 0), ([], 100, 0)])
+def test_rows_of_no_sequence(lens, front, tail):
+    """Rows in front of the first packed sequence and behind the last, also where sequences are cut:
+    the forward leaves them, the training forward and the gradients have zeros there."""
+    import gated_delta_rule_36_amd as G
+    from gated_delta_rule_36_amd import _attn
+    D = 72
+    v, g, w, s0, cu, rng = _case(16, 1, 0, D, "fp32", lens=lens, front=front, tail=tail, decay=0.01)
+    N, T = len(lens), v.shape[1]
+    do, ds = draw(rng, *v.shape, dtype=torch.float32).cuda(), torch.randn(N, D, device="cuda")
+    inside = torch.zeros(T, dtype=torch.bool, device="cuda")
+    inside[front:T - tail] = bool(lens)
+    v[:, ~inside] = float("nan")
+    do[:, ~inside] = float("nan")
+    say("linear_recurrence rows of no sequence", lens, front, tail)
+    o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0, cu_seqlens=_cu(cu))
+    grads = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=ds, cu_seqlens=_cu(cu))
+    kept = torch.full_like(v, 7.0)
+    need = _lib_workspace(T, D, N)
+    ws = torch.empty(max(need, 4) // 4, device="cuda")
+    _attn._call("gdn2_linear_recurrence", v.device, v.data_ptr(), g.data_ptr(), w.data_ptr(), s0.data_ptr() or None, kept.data_ptr(),
+                None, None, _cu(cu).data_ptr(), 1, T, D, N, D, D, D, 1, ws.data_ptr(), need)
+    torch.cuda.synchronize()
+    assert (kept[0, ~inside] == 7).all() and torch.equal(kept[0, inside], o[0, inside])
+    for x in (o, *grads[:3]):
+        assert not x[0, ~inside].any()
+    vn, dn = np.nan_to_num(f64(v)), np.nan_to_num(f64(do))
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(vn, f64(g), f64(w), f64(s0), cu, torch.float32)
+    ins = inside.cpu().numpy()
+    assert_within("o", o[:, inside], ref[:, ins], bound[:, ins])
+    assert_within("last", last, lref, lbound)
+    for x, (r, b) in zip(grads, recurrence_grad_bounds(vn, f64(g), f64(w), dn, f64(s0), f64(ds), cu, torch.float32)):
+        assert_within("gradient", x, r, b)
+
+
+def _lib_workspace(T, D, N):
+    from gated_delta_rule_36_amd import _lib
+    return int(_lib.lib().gdn2_linear_recurrence_workspace_bytes(0, 1, 1, T, D, N))
 
 
 def test_resets_and_empty_batches():

@@ -42,7 +42,8 @@ def test_recurrence_refusals(what):
                 (1, dict(P=-1)), (1, dict(idx=M2)), (1, dict(com=M2)), (1, dict(steps=M4)), (1, dict(N=1 << 16, L=1 << 16, P=1 << 16))]
     else:
         bad += [(1, dict(N=3)), (1, dict(B=-1, N=-1)), (1, dict(T=-1)), (1, dict(cu=F)), (1, dict(cu=M2, B=1)),
-                (1, dict(B=1 << 16, N=1 << 16, T=1 << 16))]
+                (1, dict(B=1 << 16, N=1 << 16, T=1 << 16)), (1, dict(B=1 << 23, N=1 << 23, T=1)),
+                (1, dict(cu=F, B=1, N=(1 << 31) - 1, T=1000))]
     if what == "fwd":
         bad += [(1, dict(o=None, st=None)), (1, dict(o=M4)), (1, dict(s0=M4)), (1, dict(sN=M4)), (1, dict(st=M4))]
     if what == "bwd":
@@ -99,7 +100,7 @@ def _norm(bwd=False, **kw):
 
 @pytest.mark.parametrize("bwd", [False, True])
 def test_norm_refusals(bwd):
-    bad = [(1, dict(dtype=3)), (1, dict(rt=2)), (2, dict(dtype=1, rt=0)), (1, dict(rows=-1)), (1, dict(rows=1 << 31)),
+    bad = [(1, dict(dtype=3)), (1, dict(rt=2)), (2, dict(dtype=1, rt=0)), (1, dict(rows=-1)), (1, dict(rows=1 << 31)), (1, dict(rows=1 << 23)),
            (1, dict(D=0)), (2, dict(D=60)), (2, dict(D=16392, xs=16392, rs=16392, hs=16392)), (1, dict(eps=-1.0)),
            (1, dict(eps=math.nan)), (1, dict(eps=math.inf)), (1, dict(w=None)), (1, dict(w=M4)), (1, dict(h=None)), (1, dict(h=M4))]
     if bwd:
@@ -135,7 +136,7 @@ def test_verify_refusals():
                        (1, dict(L=(1 << 20) + 1)), (1, dict(p=None)), (1, dict(x=None)), (1, dict(u=None)), (1, dict(t=None)),
                        (1, dict(c=None)), (1, dict(p=M2)), (1, dict(q=M2)), (1, dict(dtype=0, p=0x100001)), (1, dict(x=M2)),
                        (1, dict(dl=M2)), (1, dict(u=M2)), (1, dict(t=M2)), (1, dict(c=M2)), (1, dict(ws=M4)),
-                       (3, dict(ws=None)), (3, dict(wsz=need - 1)), (1, dict(N=1 << 20, V=1 << 28))]:
+                       (3, dict(ws=None)), (3, dict(wsz=need - 1)), (1, dict(N=1 << 20, V=1 << 28)), (1, dict(N=1 << 23))]:
         assert _verify(**kw) == status, kw
     assert _verify(N=0, p=None, q=None, x=None, u=None, t=None, c=None, ws=None) == 0
 
