@@ -71,6 +71,74 @@ __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
   return p;
 }
 
+// The 8 channels of a lane in its strip: 4 from `lo` on and 4 from `hi` on, so that 8 lanes' accesses of
+// 16 bytes make one line: 8 in a row in bf16, in fp32 4 of each half of the strip. `own`: of the 64
+// channels in the order of the lanes (8 cg + c), the place in the strip.
+template <typename T>
+struct Channels {
+  int lo, hi;           // places in the strip
+  bool in_lo, in_hi;    // inside the D channels
+  int load_lo, load_hi; // lanes past the channels load some of the last ones
+  __device__ __forceinline__ Channels(int cg, int strip, int D) {
+    lo = sizeof(T) == 2 ? cg * 8 : cg * 4;
+    hi = sizeof(T) == 2 ? cg * 8 + 4 : 32 + cg * 4;
+    in_lo = strip + lo < D;
+    in_hi = strip + hi < D;
+    load_lo = in_lo ? lo : D - (sizeof(T) == 2 ? 8 : 4) - strip;
+    load_hi = in_hi ? hi : D - 4 - strip;
+  }
+  static __device__ __forceinline__ int place(int own) {
+    return sizeof(T) == 2 ? own : (own >> 3) * 4 + (own & 3) + (own & 4) * 8;
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void load(Vec8<T>& r, const T* p) const {  // p: the strip in a row
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    const u4* a = reinterpret_cast<const u4*>(p + load_lo);
+    if constexpr (sizeof(T) == 2) {
+      r.r = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(a) : *a);
+    } else {
+      const u4* b = reinterpret_cast<const u4*>(p + load_hi);
+      r.r0 = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(a) : *a);
+      r.r1 = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(b) : *b);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, const float* f) const {
+    if constexpr (sizeof(T) == 2) {
+      if (in_lo) store8_stream(p + lo, f);
+    } else {
+      if (in_lo) __builtin_nontemporal_store(f4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f4*>(p + lo));
+      if (in_hi) __builtin_nontemporal_store(f4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f4*>(p + hi));
+    }
+  }
+  // the same channels of an array in fp32
+  __device__ __forceinline__ void load_f(const float* p, float* f) const {
+    const int second = sizeof(T) == 2 ? load_lo + 4 : load_hi;
+    const f4 x = *reinterpret_cast<const f4*>(p + load_lo), y = *reinterpret_cast<const f4*>(p + second);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[i] = x[i]; f[4 + i] = y[i]; }
+  }
+  __device__ __forceinline__ void store_f(float* p, const float* f) const {
+    if (in_lo) *reinterpret_cast<f4*>(p + lo) = f4{f[0], f[1], f[2], f[3]};
+    if (in_hi) *reinterpret_cast<f4*>(p + hi) = f4{f[4], f[5], f[6], f[7]};
+  }
+};
+
+// The workgroup's (unit, strip). Where rows do not begin at lines, neighbouring strips share lines, and
+// each XCD (workgroups start on them in turn) takes a run of neighbours so that its L2 holds them once:
+// the grid is rounded up to a multiple of 8, and false says that this workgroup has nothing.
+__device__ __forceinline__ bool my_group(const RecurrenceArgs& a, int units, int& unit, int& strip) {
+  const int strips = (a.D + kStrip - 1) / kStrip;
+  int i = blockIdx.x;
+  if (a.shared_lines) {
+    const int each = gridDim.x >> 3;
+    i = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+    if (i >= units * strips) return false;
+  }
+  unit = i / strips;
+  strip = i % strips * kStrip;
+  return true;
+}
+
 // x of the lower and of the upper half of every group of 2 STEP lanes, in all of its lanes at the
 // same place (STEP 8: the halves of a 16-lane row).
 template <int STEP>
@@ -127,12 +195,12 @@ __device__ __forceinline__ void scan_level_both(int lane, float* A, float* H, fl
   }
 }
 
-// x, a value of the lane's own channel `c` of the strip, through the maps of segments [s0, s1) of a
+// x, a value of the lane's own channel `c`, through the maps of segments [s0, s1) of a
 // sequence whose units begin at `unit`: the runs take some segments each, in the order of time (BACK:
 // against it). s_map: [A, H][wave][channel].
-template <bool BACK, int NW>
-__device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit, int s0, int s1, int chl, int lane,
-                                              int run, int c, float* s_map, float& x) {
+template <bool BACK, int NW, typename T>
+__device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit, int s0, int s1, int strip, const Channels<T>& cn,
+                                              int lane, int run, int c, float* s_map, float& x) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), cg = lane & 7;
   const int each = (s1 - s0 + NW * 8 - 1) / (NW * 8);
   float A[8], H[8], XA[8], XH[8];
@@ -141,10 +209,10 @@ __device__ __forceinline__ void fold_segments(const RecurrenceArgs& a, int unit,
   for (int i = 0; i < each; ++i) {
     const int k = run * each + i;
     if (k >= s1 - s0) break;
-    const float* m = a.cut.maps + (long)(unit + (BACK ? s1 - 1 - k : s0 + k)) * 2 * a.D + chl;
+    const float* m = a.cut.maps + (long)(unit + (BACK ? s1 - 1 - k : s0 + k)) * 2 * a.D + strip;
     float ma[8], mh[8];
-    load8f(m, ma);
-    load8f(m + a.D, mh);
+    cn.load_f(m, ma);
+    cn.load_f(m + a.D, mh);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       A[j] *= ma[j];
@@ -172,21 +240,21 @@ struct Raw {
 }  // namespace
 
 // Rows t0 + row of up to ARRAYS inputs: a uniform base and one 32-bit offset a lane (strides are at most
-// kMaxStride, so that the rows of a tile stay within it).
+// kMaxStride, so that the rows of a tile stay within it). At an instant each array is at another of the
+// run's tokens.
 template <typename T, int ARRAYS>
 struct Rows {
-  const T* src[ARRAYS];  // uniform: the strip's first channel in the sequence's first row
+  const T* src[ARRAYS];  // uniform: the strip in the sequence's first row
   long stride[ARRAYS];
-  int ch;                // the lane's channel in the strip
-  template <int R>
-  __device__ __forceinline__ void load(Raw<T, R, ARRAYS>& r, int t0, int row0, int rows) const {
+  template <bool STREAM, int R>
+  __device__ __forceinline__ void load(Raw<T, R, ARRAYS>& r, const Channels<T>& cn, int t0, int row0, int rows) const {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k) {
         const int i = (j + k) % R;
         const int row = row0 + i < rows ? row0 + i : rows - 1;
-        load_stream(r.x[k][i], src[k] + t0 * stride[k] + ((unsigned)__umul24(row, (int)stride[k]) + ch));
+        cn.template load<STREAM>(r.x[k][i], src[k] + t0 * stride[k] + (unsigned)__umul24(row, (int)stride[k]));
       }
     }
   }
@@ -194,37 +262,35 @@ struct Rows {
 
 // Zeros in the rows of a packed batch that belong to no sequence, 64 channels a workgroup.
 template <typename T>
-__device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, int ch, bool live) {
+__device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, const Channels<T>& cn, int strip) {
   const int first = clamped_offset(a.cu_seqlens, 0, a.T), last = clamped_offset(a.cu_seqlens, a.N, a.T);
   const float zero[8] = {};
   for (int t = threadIdx.x >> 3; t < a.T; t += blockDim.x >> 3)
-    if (live && (t < first || t >= last)) store8(x + (long)t * a.D + ch, zero);
+    if (t < first || t >= last) cn.store(x + (long)t * a.D + strip, zero);
 }
 
 // One workgroup a (unit, 64 channels), and where states are kept for the backward of a packed batch one
 // row of them more, for the rows of no sequence. A tile's registers are filled with the next tile's inputs as
 // soon as its values are widened to fp32, so that loads are in flight during the scan and the stores.
-template <typename T, bool GATE, int NW>
+template <typename T, bool GATE, int NW, bool STREAM>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs a) {
   constexpr int R = run_tokens<T>(), TILE = NW * 8 * R, NA = GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][2][NW][kStrip];  // [parity][A, H][wave][channel]
   __shared__ __attribute__((aligned(16))) float s_in[NW][kStrip];         // the state before a wave's runs
-  const int strips = (a.D + kStrip - 1) / kStrip;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
+  int unit, strip;
+  if (!my_group(a, a.cut.units + a.zero_rest, unit, strip)) return;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
-  const int ch = strip + cg * 8;
-  const bool live = ch < a.D;
+  const Channels<T> cn(cg, strip, a.D);
   if (unit == a.cut.units) {
-    zero_outside(a, (T*)a.o, ch, live);
+    zero_outside(a, (T*)a.o, cn, strip);
     return;
   }
   const Piece p = piece_of(a, unit);
   if (p.begin > p.end) return;
-  const int chl = live ? ch : a.D - 8;  // lanes past the channels load some of the last ones
   // the channel whose state this lane carries from tile to tile
-  const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
+  const int own = cg * 8 + (lane >> 3), owned = strip + Channels<T>::place(own), och = owned < a.D ? owned : a.D - 1;
   Rows<T, NA> in;
   in.src[0] = (const T*)a.v + p.first * a.v_stride + strip;
   in.src[1] = (const T*)a.g + p.first * a.g_stride + strip;
@@ -234,12 +300,11 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
     in.src[2] = (const T*)a.w + p.first * a.w_stride + strip;
     in.stride[2] = a.w_stride;
   }
-  in.ch = chl - strip;
   T* const out = a.o != nullptr ? (T*)a.o + p.first * a.D + strip : nullptr;
-  float* const kept = a.states != nullptr ? a.states + p.slot * a.D + ch : nullptr;
+  float* const kept = a.states != nullptr ? a.states + p.slot * a.D + strip : nullptr;
 
   Raw<T, R, NA> r;
-  if (p.begin < p.end) in.load(r, p.begin, run * R, p.end - p.begin);
+  if (p.begin < p.end) in.template load<STREAM>(r, cn, p.begin, run * R, p.end - p.begin);
   // The initial state goes through LDS from the lanes that write the final one, which may be the same
   // memory.
   float h = 0.f;
@@ -250,7 +315,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   }
   int parity = 0;
   if (p.index > 0) {  // the maps of the segments before this one
-    fold_segments<false, NW>(a, unit - p.index, 0, p.index, chl, lane, run, own, &s_map[0][0][0][0], h);
+    fold_segments<false, NW>(a, unit - p.index, 0, p.index, strip, cn, lane, run, own, &s_map[0][0][0][0], h);
     parity = 1;
   }
   for (int t0 = p.begin; t0 < p.end; t0 += TILE) {
@@ -274,7 +339,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
         H[c] = fmaf(al[i][c], H[c], z[i][c]);
       }
     }
-    if (t0 + TILE < p.end) in.load(r, t0 + TILE, run * R, p.end - t0 - TILE);
+    if (t0 + TILE < p.end) in.template load<STREAM>(r, cn, t0 + TILE, run * R, p.end - t0 - TILE);
 #pragma unroll
     for (int c = 0; c < 8; ++c) A[c] = fast_exp2(A[c]);
     scan_level<8>(lane, A, H, XA, XH);
@@ -300,18 +365,18 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
 #pragma unroll
     for (int c = 0; c < 8; ++c) x[c] = fmaf(XA[c], x[c], XH[c]);
     const int t = t0 + run * R;
-    if (kept != nullptr && live && mine > 0 && t % kStateTokens == 0) store8(kept + (long)(t / kStateTokens) * a.D, x);
+    if (kept != nullptr && mine > 0 && t % kStateTokens == 0) cn.store_f(kept + (long)(t / kStateTokens) * a.D, x);
     if (out != nullptr) {
       T* const to = out + (long)t0 * a.D;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = fmaf(al[i][c], x[c], z[i][c]);
-        if (live && i < mine) store8_stream(to + ((unsigned)__umul24(run * R + i, a.D) + cg * 8), x);
+        if (i < mine) cn.store(to + (unsigned)__umul24(run * R + i, a.D), x);
       }
     }
   }
-  if (a.sN != nullptr && p.end == p.len && wave == 0 && strip + own < a.D) a.sN[(long)p.n * a.D + och] = h;
+  if (a.sN != nullptr && p.end == p.len && wave == 0 && owned < a.D) a.sN[(long)p.n * a.D + och] = h;
 }
 
 // The maps of the segments of long sequences, which run in parallel where sequences and channels
@@ -322,14 +387,13 @@ template <typename T, bool GATE, bool BACK>
 __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArgs a, const T* d_o) {
   constexpr int AHEAD = 4, NA = !BACK && GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][kRuns][kStrip];
-  const int strips = (a.D + kStrip - 1) / kStrip;
-  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
+  int unit, strip;
+  if (!my_group(a, a.cut.units, unit, strip)) return;
   const Piece p = piece_of(a, unit);
   if (p.begin >= p.end || (BACK ? p.begin == 0 : p.end == p.len)) return;
   const int cg = threadIdx.x & 7, run = threadIdx.x >> 3;
-  const int ch = strip + cg * 8;
-  const int chl = ch < a.D ? ch : a.D - 8;
-  const T* src[3] = {(const T*)a.g + chl, BACK ? d_o + chl : (const T*)a.v + chl, GATE ? (const T*)a.w + chl : nullptr};
+  const Channels<T> cn(cg, strip, a.D);
+  const T* src[3] = {(const T*)a.g + strip, (BACK ? d_o : (const T*)a.v) + strip, GATE ? (const T*)a.w + strip : nullptr};
   const long stride[3] = {a.g_stride, BACK ? (long)a.D : a.v_stride, a.w_stride};
   const int each = a.cut.seg / kRuns;
   // tokens t0, t0 + 1, .. (BACK: t0, t0 - 1, ..), those past the end counting as none
@@ -344,7 +408,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
       t = t < p.end ? t : p.end - 1;
       t = t > 0 ? t : 0;
 #pragma unroll
-      for (int k = 0; k < NA; ++k) r.x[k][i].load(src[k] + (p.first + t) * stride[k]);
+      for (int k = 0; k < NA; ++k) cn.template load<false>(r.x[k][i], src[k] + (p.first + t) * stride[k]);
     }
   };
   Raw<T, AHEAD, NA> cur, next;
@@ -376,7 +440,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
   store8(&s_map[1][run][cg * 8], H);
   lds_barrier();
   if (threadIdx.x < kStrip) {
-    const int c = strip + threadIdx.x;
+    const int c = strip + Channels<T>::place(threadIdx.x);
     float A = 1.f, B = 0.f;
 #pragma unroll 8
     for (int k = 0; k < kRuns; ++k) {
@@ -394,30 +458,28 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
 // Gradients, tiles from the last to the first: the states come from the kept ones, the carry e runs
 // against time. One more workgroup row behind the units (packed batches) writes zeros to the
 // gradients of rows that belong to no sequence.
-template <typename T, bool GATE, int NW>
+template <typename T, bool GATE, int NW, bool STREAM>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(RecurrenceBwdArgs b) {
   constexpr int R = 2, TILE = NW * 8 * R, NA = GATE ? 4 : 3;
   static_assert(TILE % kStateTokens == 0, "a tile starts at a kept state");
   __shared__ __attribute__((aligned(16))) float s_map[2][3][NW][kStrip];  // [parity][A, H, L][wave][channel]
   __shared__ __attribute__((aligned(16))) float s_in[2][NW][kStrip];      // the state before a wave's runs, the gradient behind
   const RecurrenceArgs& a = b.f;
-  const int strips = (a.D + kStrip - 1) / kStrip;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = blockIdx.x / strips, strip = blockIdx.x % strips * kStrip;
+  int unit, strip;
+  if (!my_group(a, a.cut.units + a.zero_rest, unit, strip)) return;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
-  const int ch = strip + cg * 8;
-  const bool live = ch < a.D;
-  const int chl = live ? ch : a.D - 8;
-  const int own = cg * 8 + (lane >> 3), och = strip + own < a.D ? strip + own : a.D - 1;
+  const Channels<T> cn(cg, strip, a.D);
   if (unit == a.cut.units) {
-    zero_outside(a, (T*)b.dv, ch, live);
-    zero_outside(a, (T*)b.dg, ch, live);
-    if (GATE) zero_outside(a, (T*)b.dw, ch, live);
+    zero_outside(a, (T*)b.dv, cn, strip);
+    zero_outside(a, (T*)b.dg, cn, strip);
+    if (GATE) zero_outside(a, (T*)b.dw, cn, strip);
     return;
   }
   const Piece p = piece_of(a, unit);
   if (p.begin > p.end) return;
+  const int own = cg * 8 + (lane >> 3), owned = strip + Channels<T>::place(own), och = owned < a.D ? owned : a.D - 1;
   Rows<T, NA> in;
   in.src[0] = (const T*)a.v + p.first * a.v_stride + strip;
   in.src[1] = (const T*)a.g + p.first * a.g_stride + strip;
@@ -429,7 +491,6 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
     in.src[3] = (const T*)a.w + p.first * a.w_stride + strip;
     in.stride[3] = a.w_stride;
   }
-  in.ch = chl - strip;
   const float* const kept = a.states + p.slot * a.D + och;
   const long out = p.first * a.D + strip;
 
@@ -438,14 +499,14 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
   int parity = 0;
   Raw<T, R, NA> r;
   auto load = [&](int t0) {
-    in.load(r, t0, run * R, p.end - t0);
+    in.template load<STREAM>(r, cn, t0, run * R, p.end - t0);
     hnext = kept[(long)(t0 / kStateTokens) * a.D];
   };
   const int t_last = p.begin + (p.end - 1 - p.begin) / TILE * TILE;
   if (p.begin < p.end) load(t_last);
   if (p.end < p.len) {  // the maps of the segments behind this one
     const int count = (p.len + a.cut.seg - 1) / a.cut.seg;
-    fold_segments<true, NW>(a, unit - p.index, p.index + 1, count, chl, lane, run, own, &s_map[0][0][0][0], e);
+    fold_segments<true, NW>(a, unit - p.index, p.index + 1, count, strip, cn, lane, run, own, &s_map[0][0][0][0], e);
     parity = 1;
   }
   for (int t0 = t_last; p.begin < p.end && t0 >= p.begin; t0 -= TILE) {
@@ -536,15 +597,15 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
         gw[c] = dt * v[c];
         gg[c] = y[c] * before[i][c];
       }
-      if (live && i < mine) {
-        const unsigned at = (unsigned)__umul24(run * R + i, a.D) + cg * 8;
-        store8_stream((T*)b.dv + at0 + at, gv);
-        store8_stream((T*)b.dg + at0 + at, gg);
-        if constexpr (GATE) store8_stream((T*)b.dw + at0 + at, gw);
+      if (i < mine) {
+        const unsigned at = (unsigned)__umul24(run * R + i, a.D);
+        cn.store((T*)b.dv + at0 + at, gv);
+        cn.store((T*)b.dg + at0 + at, gg);
+        if constexpr (GATE) cn.store((T*)b.dw + at0 + at, gw);
       }
     }
   }
-  if (b.d_s0 != nullptr && p.begin == 0 && wave == 0 && strip + own < a.D) b.d_s0[(long)p.n * a.D + och] = e;
+  if (b.d_s0 != nullptr && p.begin == 0 && wave == 0 && owned < a.D) b.d_s0[(long)p.n * a.D + och] = e;
 }
 
 // L tokens of every sequence against a pool of states: a lane takes 8 channels of one sequence, its
@@ -633,7 +694,7 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
   c.units = packed ? (int)(T / seg) + N : N * c.per_sequence;
   return c;
 }
-long recurrence_groups(const RecurrenceCut& c, int D) { return ((long)c.units + 1) * strips_of(D); }
+long recurrence_groups(const RecurrenceCut& c, int D) { return ((long)c.units + 1) * strips_of(D) + 7; }
 size_t recurrence_workspace_bytes(const RecurrenceCut& c, int D) {
   return c.cut ? (size_t)c.units * 2 * D * sizeof(float) : 0;
 }
@@ -645,33 +706,66 @@ namespace {
 // backward in fp32 has no registers for it.)
 bool wide_groups(const RecurrenceCut& c, int strips) { return !c.cut && (long)c.units * strips <= 512; }
 
-template <typename T, bool GATE>
-hipError_t forward(const RecurrenceArgs& a) {
+// Whether rows begin at lines of 128 bytes.
+bool at_lines(const void* p, long stride, size_t size) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 128 == 0 && stride * size % 128 == 0);
+}
+// Inputs of more than half the Infinity Cache (256 MB), at lines, are read past the caches: 8 x 2048
+// tokens of 2048 channels in bf16 60 -> 57 us; of half as many, where repeated calls find them there,
+// 26 -> 30. Rows that share lines lose by it (7 packed sequences of 520 channels in fp32 29 -> 37).
+bool streamed(const RecurrenceArgs& a, long tokens, int arrays, size_t size) {
+  return !a.shared_lines && tokens * a.D * arrays * (long)size > (128L << 20);
+}
+unsigned grid_of(const RecurrenceArgs& a, int units) {
+  const long n = (long)units * strips_of(a.D);
+  return (unsigned)(a.shared_lines ? (n + 7) / 8 * 8 : n);
+}
+
+template <typename T, bool GATE, bool STREAM>
+void launch_forward(const RecurrenceArgs& a) {
   const hipStream_t st = (hipStream_t)a.stream;
-  const int strips = strips_of(a.D);
-  const bool rest = a.cu_seqlens != nullptr && a.states != nullptr && a.o != nullptr;  // rows of no sequence
-  const dim3 grid((unsigned)((a.cut.units + rest) * strips));
-  if (a.cut.cut) hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3((unsigned)(a.cut.units * strips)), dim3(256), 0, st, a, (const T*)nullptr);
-  if (wide_groups(a.cut, strips)) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8>), grid, dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4>), grid, dim3(256), 0, st, a);
+  const dim3 grid(grid_of(a, a.cut.units + a.zero_rest));
+  if (wide_groups(a.cut, strips_of(a.D))) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, STREAM>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4, STREAM>), grid, dim3(256), 0, st, a);
+}
+template <typename T, bool GATE>
+hipError_t forward(RecurrenceArgs a) {
+  const long tokens = a.cu_seqlens != nullptr ? a.T : (long)a.N * a.T;
+  a.zero_rest = a.cu_seqlens != nullptr && a.states != nullptr && a.o != nullptr;
+  a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
+                   !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(a.o, a.D, sizeof(T));
+  if (a.cut.cut)
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
+                       (hipStream_t)a.stream, a, (const T*)nullptr);
+  if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T))) launch_forward<T, GATE, true>(a);
+  else launch_forward<T, GATE, false>(a);
   return hipGetLastError();
 }
 
-template <typename T, bool GATE>
-hipError_t backward(const RecurrenceBwdArgs& b) {
-  const RecurrenceArgs& a = b.f;
-  const hipStream_t st = (hipStream_t)a.stream;
-  const int strips = strips_of(a.D);
-  if (a.cut.cut)
-    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3((unsigned)(a.cut.units * strips)), dim3(256), 0, st, a, (const T*)b.d_o);
-  const dim3 grid((unsigned)((a.cut.units + (a.cu_seqlens != nullptr)) * strips));  // the last row: rows of no sequence
+template <typename T, bool GATE, bool STREAM>
+void launch_backward(const RecurrenceBwdArgs& b) {
+  const hipStream_t st = (hipStream_t)b.f.stream;
+  const dim3 grid(grid_of(b.f, b.f.cut.units + b.f.zero_rest));
   if constexpr (sizeof(T) == 2) {
-    if (wide_groups(a.cut, strips)) {
-      hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 8>), grid, dim3(512), 0, st, b);
-      return hipGetLastError();
+    if (wide_groups(b.f.cut, strips_of(b.f.D))) {
+      hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 8, STREAM>), grid, dim3(512), 0, st, b);
+      return;
     }
   }
-  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 4>), grid, dim3(256), 0, st, b);
+  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 4, STREAM>), grid, dim3(256), 0, st, b);
+}
+template <typename T, bool GATE>
+hipError_t backward(RecurrenceBwdArgs b) {
+  RecurrenceArgs& a = b.f;
+  const long tokens = a.cu_seqlens != nullptr ? a.T : (long)a.N * a.T;
+  a.zero_rest = a.cu_seqlens != nullptr;
+  a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
+                   !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(b.d_o, a.D, sizeof(T));
+  if (a.cut.cut)
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
+                       (hipStream_t)a.stream, a, (const T*)b.d_o);
+  if (streamed(a, tokens, GATE ? 4 : 3, sizeof(T))) launch_backward<T, GATE, true>(b);
+  else launch_backward<T, GATE, false>(b);
   return hipGetLastError();
 }
 

@@ -31,6 +31,8 @@ struct RecurrenceArgs {
   long v_stride, g_stride, w_stride;
   int T, N, D, dtype;         // T: tokens of a sequence, or in all when packed
   RecurrenceCut cut;
+  bool zero_rest;             // set by the launchers: zeros to the rows of no sequence,
+  bool shared_lines;          // rows that do not begin at lines of 128 bytes
   void* stream;
 };
 struct RecurrenceBwdArgs {
