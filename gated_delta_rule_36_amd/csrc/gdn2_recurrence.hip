@@ -71,6 +71,11 @@ __device__ __forceinline__ Piece piece_of(const RecurrenceArgs& a, int u) {
   return p;
 }
 
+// What a launch knows of its rows. Lines of 128 bytes that two strips share stay in the caches, for
+// both loads and stores; outputs in whole lines go past them; inputs too where they are too many to
+// be there (see streamed()).
+enum { kSharedLines = 0, kLines = 1, kStream = 2 };
+
 // The 8 channels of a lane in its strip: 4 from `lo` on and 4 from `hi` on, so that 8 lanes' accesses of
 // 16 bytes make one line: 8 in a row in bf16, in fp32 4 of each half of the strip. `own`: of the 64
 // channels in the order of the lanes (8 cg + c), the place in the strip.
@@ -90,20 +95,25 @@ struct Channels {
   static __device__ __forceinline__ int place(int own) {
     return sizeof(T) == 2 ? own : (own >> 3) * 4 + (own & 3) + (own & 4) * 8;
   }
-  template <bool STREAM>
+  template <int MODE>
   __device__ __forceinline__ void load(Vec8<T>& r, const T* p) const {  // p: the strip in a row
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
     const u4* a = reinterpret_cast<const u4*>(p + load_lo);
     if constexpr (sizeof(T) == 2) {
-      r.r = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(a) : *a);
+      r.r = __builtin_bit_cast(uint4, MODE == kStream ? __builtin_nontemporal_load(a) : *a);
     } else {
       const u4* b = reinterpret_cast<const u4*>(p + load_hi);
-      r.r0 = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(a) : *a);
-      r.r1 = __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(b) : *b);
+      r.r0 = __builtin_bit_cast(uint4, MODE == kStream ? __builtin_nontemporal_load(a) : *a);
+      r.r1 = __builtin_bit_cast(uint4, MODE == kStream ? __builtin_nontemporal_load(b) : *b);
     }
   }
+  template <int MODE>
   __device__ __forceinline__ void store(T* p, const float* f) const {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (MODE == kSharedLines && sizeof(T) == 2) {
+      if (in_lo) store8(p + lo, f);
+    } else if constexpr (MODE == kSharedLines) {
+      store_f(p, f);
+    } else if constexpr (sizeof(T) == 2) {
       if (in_lo) store8_stream(p + lo, f);
     } else {
       if (in_lo) __builtin_nontemporal_store(f4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f4*>(p + lo));
@@ -246,7 +256,7 @@ template <typename T, int ARRAYS>
 struct Rows {
   const T* src[ARRAYS];  // uniform: the strip in the sequence's first row
   long stride[ARRAYS];
-  template <bool STREAM, int R>
+  template <int MODE, int R>
   __device__ __forceinline__ void load(Raw<T, R, ARRAYS>& r, const Channels<T>& cn, int t0, int row0, int rows) const {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -254,7 +264,7 @@ struct Rows {
       for (int k = 0; k < ARRAYS; ++k) {
         const int i = (j + k) % R;
         const int row = row0 + i < rows ? row0 + i : rows - 1;
-        cn.template load<STREAM>(r.x[k][i], src[k] + t0 * stride[k] + (unsigned)__umul24(row, (int)stride[k]));
+        cn.template load<MODE>(r.x[k][i], src[k] + t0 * stride[k] + (unsigned)__umul24(row, (int)stride[k]));
       }
     }
   }
@@ -266,13 +276,13 @@ __device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, cons
   const int first = clamped_offset(a.cu_seqlens, 0, a.T), last = clamped_offset(a.cu_seqlens, a.N, a.T);
   const float zero[8] = {};
   for (int t = threadIdx.x >> 3; t < a.T; t += blockDim.x >> 3)
-    if (t < first || t >= last) cn.store(x + (long)t * a.D + strip, zero);
+    if (t < first || t >= last) cn.template store<kSharedLines>(x + (long)t * a.D + strip, zero);
 }
 
 // One workgroup a (unit, 64 channels), and where states are kept for the backward of a packed batch one
 // row of them more, for the rows of no sequence. A tile's registers are filled with the next tile's inputs as
 // soon as its values are widened to fp32, so that loads are in flight during the scan and the stores.
-template <typename T, bool GATE, int NW, bool STREAM>
+template <typename T, bool GATE, int NW, int MODE>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs a) {
   constexpr int R = run_tokens<T>(), TILE = NW * 8 * R, NA = GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][2][NW][kStrip];  // [parity][A, H][wave][channel]
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   float* const kept = a.states != nullptr ? a.states + p.slot * a.D + strip : nullptr;
 
   Raw<T, R, NA> r;
-  if (p.begin < p.end) in.template load<STREAM>(r, cn, p.begin, run * R, p.end - p.begin);
+  if (p.begin < p.end) in.template load<MODE>(r, cn, p.begin, run * R, p.end - p.begin);
   // The initial state goes through LDS from the lanes that write the final one, which may be the same
   // memory.
   float h = 0.f;
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
         H[c] = fmaf(al[i][c], H[c], z[i][c]);
       }
     }
-    if (t0 + TILE < p.end) in.template load<STREAM>(r, cn, t0 + TILE, run * R, p.end - t0 - TILE);
+    if (t0 + TILE < p.end) in.template load<MODE>(r, cn, t0 + TILE, run * R, p.end - t0 - TILE);
 #pragma unroll
     for (int c = 0; c < 8; ++c) A[c] = fast_exp2(A[c]);
     scan_level<8>(lane, A, H, XA, XH);
@@ -372,7 +382,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) x[c] = fmaf(al[i][c], x[c], z[i][c]);
-        if (i < mine) cn.store(to + (unsigned)__umul24(run * R + i, a.D), x);
+        if (i < mine) cn.template store<MODE>(to + (unsigned)__umul24(run * R + i, a.D), x);
       }
     }
   }
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
       t = t < p.end ? t : p.end - 1;
       t = t > 0 ? t : 0;
 #pragma unroll
-      for (int k = 0; k < NA; ++k) cn.template load<false>(r.x[k][i], src[k] + (p.first + t) * stride[k]);
+      for (int k = 0; k < NA; ++k) cn.template load<kLines>(r.x[k][i], src[k] + (p.first + t) * stride[k]);
     }
   };
   Raw<T, AHEAD, NA> cur, next;
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
 // Gradients, tiles from the last to the first: the states come from the kept ones, the carry e runs
 // against time. One more workgroup row behind the units (packed batches) writes zeros to the
 // gradients of rows that belong to no sequence.
-template <typename T, bool GATE, int NW, bool STREAM>
+template <typename T, bool GATE, int NW, int MODE>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(RecurrenceBwdArgs b) {
   constexpr int R = 2, TILE = NW * 8 * R, NA = GATE ? 4 : 3;
   static_assert(TILE % kStateTokens == 0, "a tile starts at a kept state");
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
   int parity = 0;
   Raw<T, R, NA> r;
   auto load = [&](int t0) {
-    in.template load<STREAM>(r, cn, t0, run * R, p.end - t0);
+    in.template load<MODE>(r, cn, t0, run * R, p.end - t0);
     hnext = kept[(long)(t0 / kStateTokens) * a.D];
   };
   const int t_last = p.begin + (p.end - 1 - p.begin) / TILE * TILE;
@@ -599,9 +609,9 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_bwd_kernel(Recurrence
       }
       if (i < mine) {
         const unsigned at = (unsigned)__umul24(run * R + i, a.D);
-        cn.store((T*)b.dv + at0 + at, gv);
-        cn.store((T*)b.dg + at0 + at, gg);
-        if constexpr (GATE) cn.store((T*)b.dw + at0 + at, gw);
+        cn.template store<MODE>((T*)b.dv + at0 + at, gv);
+        cn.template store<MODE>((T*)b.dg + at0 + at, gg);
+        if constexpr (GATE) cn.template store<MODE>((T*)b.dw + at0 + at, gw);
       }
     }
   }
@@ -710,23 +720,24 @@ bool wide_groups(const RecurrenceCut& c, int strips) { return !c.cut && (long)c.
 bool at_lines(const void* p, long stride, size_t size) {
   return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 128 == 0 && stride * size % 128 == 0);
 }
-// Inputs of more than half the Infinity Cache (256 MB), at lines, are read past the caches: 8 x 2048
-// tokens of 2048 channels in bf16 60 -> 57 us; of half as many, where repeated calls find them there,
-// 26 -> 30. Rows that share lines lose by it (7 packed sequences of 520 channels in fp32 29 -> 37).
+// Inputs of more than half the Infinity Cache (256 MB) are read past the caches: 8 x 2048 tokens of
+// 2048 channels in bf16 60 -> 57 us; of half as many, where repeated calls find them there, 26 -> 30.
+// (Rows that share lines lose by it: 7 packed sequences of 520 channels in fp32 29 -> 37, and their
+// backward by stores past the caches, 8 x 1024 x 1000 in bf16 42 -> 51.)
 bool streamed(const RecurrenceArgs& a, long tokens, int arrays, size_t size) {
-  return !a.shared_lines && tokens * a.D * arrays * (long)size > (128L << 20);
+  return tokens * a.D * arrays * (long)size > (128L << 20);
 }
 unsigned grid_of(const RecurrenceArgs& a, int units) {
   const long n = (long)units * strips_of(a.D);
   return (unsigned)(a.shared_lines ? (n + 7) / 8 * 8 : n);
 }
 
-template <typename T, bool GATE, bool STREAM>
+template <typename T, bool GATE, int MODE>
 void launch_forward(const RecurrenceArgs& a) {
   const hipStream_t st = (hipStream_t)a.stream;
   const dim3 grid(grid_of(a, a.cut.units + a.zero_rest));
-  if (wide_groups(a.cut, strips_of(a.D))) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, STREAM>), grid, dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4, STREAM>), grid, dim3(256), 0, st, a);
+  if (wide_groups(a.cut, strips_of(a.D))) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, MODE>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4, MODE>), grid, dim3(256), 0, st, a);
 }
 template <typename T, bool GATE>
 hipError_t forward(RecurrenceArgs a) {
@@ -737,22 +748,23 @@ hipError_t forward(RecurrenceArgs a) {
   if (a.cut.cut)
     hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
                        (hipStream_t)a.stream, a, (const T*)nullptr);
-  if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T))) launch_forward<T, GATE, true>(a);
-  else launch_forward<T, GATE, false>(a);
+  if (a.shared_lines) launch_forward<T, GATE, kSharedLines>(a);
+  else if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T))) launch_forward<T, GATE, kStream>(a);
+  else launch_forward<T, GATE, kLines>(a);
   return hipGetLastError();
 }
 
-template <typename T, bool GATE, bool STREAM>
+template <typename T, bool GATE, int MODE>
 void launch_backward(const RecurrenceBwdArgs& b) {
   const hipStream_t st = (hipStream_t)b.f.stream;
   const dim3 grid(grid_of(b.f, b.f.cut.units + b.f.zero_rest));
   if constexpr (sizeof(T) == 2) {
     if (wide_groups(b.f.cut, strips_of(b.f.D))) {
-      hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 8, STREAM>), grid, dim3(512), 0, st, b);
+      hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 8, MODE>), grid, dim3(512), 0, st, b);
       return;
     }
   }
-  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 4, STREAM>), grid, dim3(256), 0, st, b);
+  hipLaunchKernelGGL((gdn2_recurrence_bwd_kernel<T, GATE, 4, MODE>), grid, dim3(256), 0, st, b);
 }
 template <typename T, bool GATE>
 hipError_t backward(RecurrenceBwdArgs b) {
@@ -764,8 +776,9 @@ hipError_t backward(RecurrenceBwdArgs b) {
   if (a.cut.cut)
     hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
                        (hipStream_t)a.stream, a, (const T*)b.d_o);
-  if (streamed(a, tokens, GATE ? 4 : 3, sizeof(T))) launch_backward<T, GATE, true>(b);
-  else launch_backward<T, GATE, false>(b);
+  if (a.shared_lines) launch_backward<T, GATE, kSharedLines>(b);
+  else if (streamed(a, tokens, GATE ? 4 : 3, sizeof(T))) launch_backward<T, GATE, kStream>(b);
+  else launch_backward<T, GATE, kLines>(b);
   return hipGetLastError();
 }
 
