@@ -75,6 +75,7 @@ struct ResidualNormArgs {
   int D, group;         // group: channels of a scale (32, 64, 128 or D)
   float eps;
   int dtype, r_dtype;   // of x and y, of r and h
+  bool stream_rows;     // set by the launcher: inputs past the caches
   void* stream;
 };
 struct ResidualNormBwdArgs {
