@@ -28,14 +28,19 @@ def _row_stride(name, t):
     """Elements from one row (of the last axis) to the next; rows dense and at one stride."""
     if t.is_contiguous():
         return t.shape[-1]
-    D = t.shape[-1]
-    try:
-        step, inner = t.view(-1, D).stride()
-    except RuntimeError:
-        step, inner = 0, 0
-    if t.numel() == D:
-        step = D  # one row: no step is taken
-    if (inner != 1 and D > 1) or step < D or step % 8:
+    *lead, D = t.shape
+    *steps, inner = t.stride()
+    step = span = 0
+    good = inner == 1 or D <= 1
+    for n, s in zip(reversed(lead), reversed(steps)):  # axes of one are skipped, others follow each other
+        if n == 1:
+            continue
+        if not step:
+            step, span = s, n * s
+        else:
+            good, span = good and s == span, n * span
+    step = step or D
+    if not good or step < D or step % 8:
         raise ValueError(f"{name}: rows must be dense and at one stride, a multiple of 8 elements, "
                          f"got strides {t.stride()} for shape {tuple(t.shape)}")
     return step
@@ -46,6 +51,18 @@ def _like(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _bad(name, t, shape, dtype, device)
     return _row_stride(name, t)
+
+
+def _no_second(backward):
+    """once_differentiable, whose own bookkeeping is skipped where no graph of the gradients is asked
+    for."""
+    recorded = torch.autograd.function.once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        return (recorded if torch.is_grad_enabled() else backward)(ctx, *grads)
+
+    return run
 
 
 # ---------------------------------------------------------------- diagonal recurrence
@@ -158,7 +175,7 @@ class _LinearRecurrence(torch.autograd.Function):
         return o, last
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_no_second
     def backward(ctx, do, d_last):
         v, g, w, states, cu = ctx.saved_tensors
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _aligned_gradient(do)
@@ -327,7 +344,7 @@ def _norm_bwd(dy, dh, h, weight, eps):
 class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps):
-        y, h = residual_norm_fwd(x, residual, weight, eps)
+        y, _, h = _norm(x, residual, weight, eps, None, None)
         ctx.set_materialize_grads(False)
         ctx.eps = eps
         ctx.save_for_backward(h, weight)
@@ -335,7 +352,7 @@ class _ResidualNorm(torch.autograd.Function):
         return y if residual is None else (y, h)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_no_second
     def backward(ctx, dy, dh=None):
         h, weight = ctx.saved_tensors
         dy = torch.zeros(h.shape, dtype=ctx.dt, device=h.device) if dy is None else _aligned_gradient(dy)

@@ -200,6 +200,18 @@ def test_recurrence_binding_refusals(anywhere):
             G.linear_recurrence_bwd(*args, **kw)
 
 
+def test_row_strides():
+    """Rows of a tensor's last axis at one stride, whatever the axes in front are."""
+    x = torch.zeros(4, 3, 5, 64)
+    for t, step in [(x, 64), (x[..., :32], 64), (x[:, :, :1], 320), (x[:, :1, :1, 8:24], 960), (x[2, 1, 3, 8:16], 8),
+                    (x[:1, :1, :1, :40], 40), (x.transpose(0, 1)[:, :1], 64), (x[1:3, :, :, 32:], 64)]:
+        assert _stack._row_stride("x", t) == step, (t.shape, t.stride())
+    for t in (x.transpose(0, 1), x[:, :, ::2, :32], x[:, ::2], x[..., ::2], x.expand(4, 3, 5, 64).transpose(-1, -2),
+              torch.zeros(2, 1, 64).expand(2, 3, 64), torch.zeros(3, 68)[:, :64], torch.zeros(4, 32).as_strided((3, 32), (16, 1))):
+        with pytest.raises(ValueError):
+            _stack._row_stride("x", t)
+
+
 def test_recurrence_tokens_binding_refusals(anywhere):
     import gated_delta_rule_36_amd as G
     v, pool, n = torch.zeros(3, 2, 64), torch.zeros(4, 64), torch.zeros(3, dtype=torch.int32)
