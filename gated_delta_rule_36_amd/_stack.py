@@ -30,16 +30,16 @@ def _row_stride(name, t):
         return t.shape[-1]
     *lead, D = t.shape
     *steps, inner = t.stride()
-    step = span = 0
+    step = span = None
     good = inner == 1 or D <= 1
     for n, s in zip(reversed(lead), reversed(steps)):  # axes of one are skipped, others follow each other
         if n == 1:
             continue
-        if not step:
+        if step is None:
             step, span = s, n * s
         else:
             good, span = good and s == span, n * span
-    step = step or D
+    step = D if step is None else step
     if not good or step < D or step % 8:
         raise ValueError(f"{name}: rows must be dense and at one stride, a multiple of 8 elements, "
                          f"got strides {t.stride()} for shape {tuple(t.shape)}")
