@@ -26,6 +26,8 @@ namespace {
 constexpr int kStrip = 64;   // channels of a workgroup
 constexpr int kRuns = 32;    // runs of 4 waves
 
+__host__ __device__ constexpr int strips_of(int D) { return (D + kStrip - 1) / kStrip; }
+
 template <typename T> constexpr int run_tokens() { return sizeof(T) == 2 ? 4 : 2; }
 
 // One piece of one sequence: all of it, or one of the segments that a long one is cut into.
@@ -137,7 +139,7 @@ struct Channels {
 // each XCD (workgroups start on them in turn) takes a run of neighbours so that its L2 holds them once:
 // the grid is rounded up to a multiple of 8, and false says that this workgroup has nothing.
 __device__ __forceinline__ bool my_group(const RecurrenceArgs& a, int units, int& unit, int& strip) {
-  const int strips = (a.D + kStrip - 1) / kStrip;
+  const int strips = strips_of(a.D);
   int i = blockIdx.x;
   if (a.shared_lines) {
     const int each = gridDim.x >> 3;
@@ -279,10 +281,21 @@ __device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, cons
     if (t < first || t >= last) cn.template store<kSharedLines>(x + (long)t * a.D + strip, zero);
 }
 
+// How a cut forward runs: the first pass walks every segment from a zero state (the first segment from
+// the initial one), leaves the segment's map h -> A h + H, and writes the outputs from the tile on in
+// front of which the decay has taken everything of what came before (A = 0 in fp32 in all channels of the
+// strip); the second pass walks the tiles before that one again, from the state that the earlier maps
+// give. 32768 tokens of 2048 channels in bf16, in us (a pass for the maps alone and one for all outputs
+// takes 178 whatever the decays are):
+//   one token in 10 a reset to e^-5       132   (every tile of a segment but the first two is final)
+//   alpha 0.92 on average                 153
+//   nothing forgotten within a segment    183   (both passes read everything: 14 bytes an element)
+enum { kWhole = 0, kFirst = 1, kSecond = 2 };
+
 // One workgroup a (unit, 64 channels), and where states are kept for the backward of a packed batch one
 // row of them more, for the rows of no sequence. A tile's registers are filled with the next tile's inputs as
 // soon as its values are widened to fp32, so that loads are in flight during the scan and the stores.
-template <typename T, bool GATE, int NW, int MODE>
+template <typename T, bool GATE, int NW, int MODE, int PASS>
 __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs a) {
   constexpr int R = run_tokens<T>(), TILE = NW * 8 * R, NA = GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][2][NW][kStrip];  // [parity][A, H][wave][channel]
@@ -290,15 +303,15 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int unit, strip;
-  if (!my_group(a, a.cut.units + a.zero_rest, unit, strip)) return;
+  if (!my_group(a, a.cut.units + (PASS != kSecond && a.zero_rest), unit, strip)) return;
   const int cg = lane & 7, run = wave * 8 + (lane >> 3);
   const Channels<T> cn(cg, strip, a.D);
-  if (unit == a.cut.units) {
+  if (PASS != kSecond && unit == a.cut.units) {
     zero_outside(a, (T*)a.o, cn, strip);
     return;
   }
   const Piece p = piece_of(a, unit);
-  if (p.begin > p.end) return;
+  if (p.begin > p.end || (PASS == kSecond && p.index == 0)) return;
   // the channel whose state this lane carries from tile to tile
   const int own = cg * 8 + (lane >> 3), owned = strip + Channels<T>::place(own), och = owned < a.D ? owned : a.D - 1;
   Rows<T, NA> in;
@@ -315,20 +328,31 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
 
   Raw<T, R, NA> r;
   if (p.begin < p.end) in.template load<MODE>(r, cn, p.begin, run * R, p.end - p.begin);
+  int end = p.end;  // of the tiles
+  // of the first pass: how much of the state before the unit is left (own channel), the tokens whose outputs still depend on it
+  float reach = p.index > 0 ? 1.f : 0.f;
+  int open = 0;
+  float* const map = PASS != kWhole ? a.cut.maps + (long)unit * 2 * a.D + och : nullptr;
+  int* const opened = PASS != kWhole ? reinterpret_cast<int*>(a.cut.maps + (long)a.cut.units * 2 * a.D) +
+                                           (long)unit * strips_of(a.D) + strip / kStrip
+                                     : nullptr;
   // The initial state goes through LDS from the lanes that write the final one, which may be the same
   // memory.
   float h = 0.f;
-  if (a.s0 != nullptr) {
+  if (PASS != kSecond && p.index == 0 && a.s0 != nullptr) {
     if (wave == 0) s_map[1][0][0][own] = a.s0[(long)p.n * a.D + och];
     lds_barrier();
     h = s_map[1][0][0][own];
   }
   int parity = 0;
-  if (p.index > 0) {  // the maps of the segments before this one
+  if constexpr (PASS == kSecond) {  // the maps of the segments before this one, the first of which starts from nothing
+    const int still = uniform(*opened);
     fold_segments<false, NW>(a, unit - p.index, 0, p.index, strip, cn, lane, run, own, &s_map[0][0][0][0], h);
     parity = 1;
+    // (a state that is not finite stays so, however far it decays)
+    if (__all(fabsf(h) < INFINITY) && still < p.end - p.begin) end = p.begin + still;
   }
-  for (int t0 = p.begin; t0 < p.end; t0 += TILE) {
+  for (int t0 = p.begin; t0 < end; t0 += TILE) {
     const int mine = p.end - (t0 + run * R);  // tokens of this run, from R down to none
     float al[R][8], z[R][8], A[8], H[8], XA[8], XH[8];
 #pragma unroll
@@ -349,7 +373,7 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
         H[c] = fmaf(al[i][c], H[c], z[i][c]);
       }
     }
-    if (t0 + TILE < p.end) in.template load<MODE>(r, cn, t0 + TILE, run * R, p.end - t0 - TILE);
+    if (t0 + TILE < end) in.template load<MODE>(r, cn, t0 + TILE, run * R, p.end - t0 - TILE);
 #pragma unroll
     for (int c = 0; c < 8; ++c) A[c] = fast_exp2(A[c]);
     scan_level<8>(lane, A, H, XA, XH);
@@ -363,13 +387,20 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
     // each lane joins the waves' maps for its own channel and hands the state before this wave's runs
     // to the lanes that hold the channel
     float xin = h;
+    const bool settled = PASS != kFirst || __all(reach == 0.f);
 #pragma unroll
     for (int u = 0; u < NW; ++u) {
+      const float wa = s_map[parity][0][u][own];
       if (u == wave) xin = h;
-      h = fmaf(s_map[parity][0][u][own], h, s_map[parity][1][u][own]);
+      h = fmaf(wa, h, s_map[parity][1][u][own]);
+      if constexpr (PASS == kFirst) reach = reach == 0.f ? 0.f : reach * wa;  // (0 stays 0, however much the decay grows)
+    }
+    parity ^= 1;
+    if (!settled) {
+      open += TILE;
+      continue;
     }
     s_in[wave][own] = xin;
-    parity ^= 1;
     float x[8];
     load8f(&s_in[wave][cg * 8], x);
 #pragma unroll
@@ -386,60 +417,61 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
       }
     }
   }
-  if (a.sN != nullptr && p.end == p.len && wave == 0 && owned < a.D) a.sN[(long)p.n * a.D + och] = h;
+  if (wave == 0 && owned < a.D) {
+    if constexpr (PASS == kFirst) {
+      map[0] = reach;
+      map[a.D] = h;
+      if (lane == 0) *opened = open;
+    }
+    // (where the second pass ended early, nothing of the state before the unit is left at its end)
+    if (a.sN != nullptr && p.end == p.len && (PASS != kFirst || p.index == 0))
+      a.sN[(long)p.n * a.D + och] = end < p.end ? map[a.D] : h;
+  }
 }
 
-// The maps of the segments of long sequences, which run in parallel where sequences and channels
-// are too few to fill the card: forward h -> A h + H of every segment that another follows, backward
-// e -> A e + L of every segment behind another. A lane walks seg / 32 consecutive tokens of 8
-// channels; the 32 runs are joined through LDS.
-template <typename T, bool GATE, bool BACK>
+// The maps e -> A e + L of the segments behind another, for the backward of long sequences. A lane walks
+// seg / 32 consecutive tokens of 8 channels, from the last to the first; the 32 runs are joined through
+// LDS.
+template <typename T>
 __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArgs a, const T* d_o) {
-  constexpr int AHEAD = 4, NA = !BACK && GATE ? 3 : 2;
+  constexpr int AHEAD = 4;
   __shared__ __attribute__((aligned(16))) float s_map[2][kRuns][kStrip];
   int unit, strip;
   if (!my_group(a, a.cut.units, unit, strip)) return;
   const Piece p = piece_of(a, unit);
-  if (p.begin >= p.end || (BACK ? p.begin == 0 : p.end == p.len)) return;
+  if (p.begin >= p.end || p.begin == 0) return;
   const int cg = threadIdx.x & 7, run = threadIdx.x >> 3;
   const Channels<T> cn(cg, strip, a.D);
-  const T* src[3] = {(const T*)a.g + strip, (BACK ? d_o : (const T*)a.v) + strip, GATE ? (const T*)a.w + strip : nullptr};
-  const long stride[3] = {a.g_stride, BACK ? (long)a.D : a.v_stride, a.w_stride};
+  const T* src[2] = {(const T*)a.g + p.first * a.g_stride + strip, d_o + p.first * a.D + strip};
+  const long stride[2] = {a.g_stride, (long)a.D};
   const int each = a.cut.seg / kRuns;
-  // tokens t0, t0 + 1, .. (BACK: t0, t0 - 1, ..), those past the end counting as none
-  const int t0 = p.begin + run * each + (BACK ? each - 1 : 0);
-  float G[8], H[8];
+  const int t0 = p.begin + run * each + each - 1;  // tokens t0, t0 - 1, .., those past the end counting as none
+  float G[8], L[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) G[c] = H[c] = 0.f;
-  auto load = [&](Raw<T, AHEAD, NA>& r, int i0) {
+  for (int c = 0; c < 8; ++c) G[c] = L[c] = 0.f;
+  auto load = [&](Raw<T, AHEAD, 2>& r, int i0) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      int t = BACK ? t0 - i0 - i : t0 + i0 + i;
-      t = t < p.end ? t : p.end - 1;
-      t = t > 0 ? t : 0;
+      const int t = t0 - i0 - i < p.end ? t0 - i0 - i : p.end - 1;
 #pragma unroll
-      for (int k = 0; k < NA; ++k) cn.template load<kLines>(r.x[k][i], src[k] + (p.first + t) * stride[k]);
+      for (int k = 0; k < 2; ++k) cn.template load<kLines>(r.x[k][i], src[k] + t * stride[k]);
     }
   };
-  Raw<T, AHEAD, NA> cur, next;
+  Raw<T, AHEAD, 2> cur, next;
   load(cur, 0);
-  for (int i0 = 0; i0 < each; i0 += AHEAD) {
+  for (int i0 = 0; i0 < each; i0 += AHEAD) {  // (each is a multiple of AHEAD)
     if (i0 + AHEAD < each) load(next, i0 + AHEAD);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const bool in = i0 + i < each && (BACK ? t0 - i0 - i : t0 + i0 + i) < p.end;
-      float g[8], x[8], w[8];
+      float g[8], x[8];
       cur.x[0][i].to_float(g);
       cur.x[1][i].to_float(x);
-      if constexpr (NA == 3) cur.x[2][i].to_float(w);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        if constexpr (NA == 3) x[c] *= w[c];
         g[c] *= kLog2e;
-        if (!in) g[c] = x[c] = 0.f;
-        const float al = fast_exp2(g[c]);
+        if (t0 - i0 - i >= p.end) g[c] = x[c] = 0.f;
         G[c] += g[c];
-        H[c] = BACK ? al * (x[c] + H[c]) : fmaf(al, H[c], x[c]);
+        L[c] = fast_exp2(g[c]) * (x[c] + L[c]);
       }
     }
     cur = next;
@@ -447,16 +479,15 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
 #pragma unroll
   for (int c = 0; c < 8; ++c) G[c] = fast_exp2(G[c]);
   store8(&s_map[0][run][cg * 8], G);
-  store8(&s_map[1][run][cg * 8], H);
+  store8(&s_map[1][run][cg * 8], L);
   lds_barrier();
   if (threadIdx.x < kStrip) {
     const int c = strip + Channels<T>::place(threadIdx.x);
     float A = 1.f, B = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < kRuns; ++k) {
-      const int r = BACK ? kRuns - 1 - k : k;
-      A *= s_map[0][r][threadIdx.x];
-      B = fmaf(s_map[0][r][threadIdx.x], B, s_map[1][r][threadIdx.x]);
+    for (int k = kRuns - 1; k >= 0; --k) {
+      A *= s_map[0][k][threadIdx.x];
+      B = fmaf(s_map[0][k][threadIdx.x], B, s_map[1][k][threadIdx.x]);
     }
     if (c < a.D) {
       a.cut.maps[(long)unit * 2 * a.D + c] = A;
@@ -669,19 +700,19 @@ long recurrence_state_slots(bool packed, int B, int T, int N) {
   return packed ? (long)T / kStateTokens + N : (long)B * ((T + kStateTokens - 1) / kStateTokens);
 }
 
-static int strips_of(int D) { return (D + kStrip - 1) / kStrip; }
-
-// A unit takes a workgroup for each of its strips, and a compute unit holds two workgroups. Uncut,
-// units are sequences: with few of them most of the card stands idle; cut, the maps' pass reads the
-// inputs once more (6 of 8 + 6 bytes an element forward, 4 of 14 + 4 backward). Measured at 2048
-// channels in bf16, 4096 tokens, forward and backward in us:
-//   sequences                 1          2          3          4          5          6
-//   uncut                 69, 140    69, 141    72, 146    76, 150    86, 158    98, 170
-//   cut                   26,  34    46,  61    66,  90    89, 112   108, 150   129, 175
-// Where workgroups run past a whole round of the card (9 sequences, 288: 80 and 145 uncut, 84 and 120
-// cut) the last round counts like a full one: cut where less than 0.44 (0.66) of the rounds is used.
-// Packed batches, whose lengths the host does not know, are cut at twice the fair share in any case,
-// for a sequence much longer than the others.
+// A unit takes a workgroup for each of its strips. Uncut, units are sequences: with few of them most of
+// the card stands idle; cut, the inputs are read once more (up to 6 of 8 + 6 bytes an element forward, see
+// the passes above; 4 of 14 + 4 backward). Measured at 2048 channels in bf16, 4096 tokens, forward (nothing
+// is forgotten) and backward in us:
+//   sequences                 1          2          3          4          5
+//   uncut                 69, 140    69, 141    72, 146    77, 150    86, 158
+//   cut                   27,  31    45,  60    64,  91    85, 113   119, 150
+// and of 6 the backward 170 uncut, 175 cut. Where workgroups run past a whole round of the card (9
+// sequences, 288: 80 and 145 uncut, 84 and 120 cut) the last round counts like a full one: cut where less
+// than 0.44 (0.66) of the rounds is used. The units fill the card: forward with one workgroup of 8 waves a
+// compute unit, since a longer segment has a larger part behind what it forgets (1 x 32768 at 256, 512 and
+// 1024 workgroups 152, 179 and 195), backward with four of 4. Packed batches, whose lengths the host does not
+// know, are cut at least into units of a 256th in any case, for a sequence much longer than the others.
 RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, int N) {
   constexpr int TILE = 128;
   RecurrenceCut c{};
@@ -690,12 +721,13 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
   c.per_sequence = 1;
   c.units = N;
   if (T < (backward ? 3 : 6) * TILE || N == 0 || N > kMaxGroups) return c;
-  long seg = ((tokens * strips + 1023) / 1024 + TILE - 1) / TILE * TILE;  // the fair share
+  const long share = backward ? 1024 : 256;
+  long seg = ((tokens * strips + share - 1) / share + TILE - 1) / TILE * TILE;  // the fair share
   if (seg < 2 * TILE) seg = 2 * TILE;
   const long rounds = (groups + 255) / 256;
   if (groups * 100 >= rounds * 256 * (backward ? 66 : 44)) {
     if (!packed) return c;
-    seg *= 4;  // of 512 workgroups
+    seg *= share / 256;
   }
   if (seg >= T) return c;
   c.cut = true;
@@ -706,7 +738,7 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
 }
 long recurrence_groups(const RecurrenceCut& c, int D) { return ((long)c.units + 1) * strips_of(D) + 7; }
 size_t recurrence_workspace_bytes(const RecurrenceCut& c, int D) {
-  return c.cut ? (size_t)c.units * 2 * D * sizeof(float) : 0;
+  return c.cut ? (size_t)c.units * (2 * D + strips_of(D)) * sizeof(float) : 0;
 }
 
 namespace {
@@ -723,9 +755,10 @@ bool at_lines(const void* p, long stride, size_t size) {
 // Inputs of more than half the Infinity Cache (256 MB) are read past the caches: 8 x 2048 tokens of
 // 2048 channels in bf16 60 -> 57 us; of half as many, where repeated calls find them there, 26 -> 30.
 // (Rows that share lines lose by it: 7 packed sequences of 520 channels in fp32 29 -> 37, and their
-// backward by stores past the caches, 8 x 1024 x 1000 in bf16 42 -> 51.)
-bool streamed(const RecurrenceArgs& a, long tokens, int arrays, size_t size) {
-  return tokens * a.D * arrays * (long)size > (128L << 20);
+// backward by stores past the caches, 8 x 1024 x 1000 in bf16 42 -> 51.) A cut forward, which reads them
+// twice, does so from the whole cache on: 16384 tokens of 2048 channels 73 -> 69.
+bool streamed(const RecurrenceArgs& a, long tokens, int arrays, size_t size, long limit = 128) {
+  return tokens * a.D * arrays * (long)size > limit << 20;
 }
 unsigned grid_of(const RecurrenceArgs& a, int units) {
   const long n = (long)units * strips_of(a.D);
@@ -736,8 +769,15 @@ template <typename T, bool GATE, int MODE>
 void launch_forward(const RecurrenceArgs& a) {
   const hipStream_t st = (hipStream_t)a.stream;
   const dim3 grid(grid_of(a, a.cut.units + a.zero_rest));
-  if (wide_groups(a.cut, strips_of(a.D))) hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, MODE>), grid, dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4, MODE>), grid, dim3(256), 0, st, a);
+  if (a.cut.cut) {  // what the first pass reads through the caches, the second finds there in part
+    constexpr int FIRST = MODE == kStream ? kLines : MODE;
+    hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, FIRST, kFirst>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, MODE, kSecond>), dim3(grid_of(a, a.cut.units)), dim3(512), 0, st, a);
+  } else if (wide_groups(a.cut, strips_of(a.D))) {
+    hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, MODE, kWhole>), grid, dim3(512), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 4, MODE, kWhole>), grid, dim3(256), 0, st, a);
+  }
 }
 template <typename T, bool GATE>
 hipError_t forward(RecurrenceArgs a) {
@@ -745,11 +785,8 @@ hipError_t forward(RecurrenceArgs a) {
   a.zero_rest = a.cu_seqlens != nullptr && a.states != nullptr && a.o != nullptr;
   a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
                    !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(a.o, a.D, sizeof(T));
-  if (a.cut.cut)
-    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
-                       (hipStream_t)a.stream, a, (const T*)nullptr);
   if (a.shared_lines) launch_forward<T, GATE, kSharedLines>(a);
-  else if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T))) launch_forward<T, GATE, kStream>(a);
+  else if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T), a.cut.cut ? 256 : 128)) launch_forward<T, GATE, kStream>(a);
   else launch_forward<T, GATE, kLines>(a);
   return hipGetLastError();
 }
@@ -774,7 +811,7 @@ hipError_t backward(RecurrenceBwdArgs b) {
   a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
                    !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(b.d_o, a.D, sizeof(T));
   if (a.cut.cut)
-    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
                        (hipStream_t)a.stream, a, (const T*)b.d_o);
   if (a.shared_lines) launch_backward<T, GATE, kSharedLines>(b);
   else if (streamed(a, tokens, GATE ? 4 : 3, sizeof(T))) launch_backward<T, GATE, kStream>(b);

@@ -33,7 +33,8 @@ def _swept(x, g, w_err, start, spans, reverse):
 # Roundings that a token meets on its way into the states behind it, of U each and of the state's
 # majorant: the gate's product 1, its own decay 3 (the logarithm's product with log2 e, |g| U, counted
 # apart; exp2 2 U) and 2 in the product and sum; then for every 2 tokens (a run in fp32; 4 in bf16) the
-# run's decay, 3, and at most 3 levels and 4 waves of products and sums, 2 x 7: 6 + 17 / 2 < 16.
+# run's decay, 3, and at most 3 levels of products and sums, 6, and for every wave in between (16 tokens or
+# more) 2, so that the number of waves does not matter: 6 + 9 / 2 + 2 / 16 < 16.
 STEP = 16 * U
 
 

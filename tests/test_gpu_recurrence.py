@@ -187,6 +187,63 @@ def test_resets_and_empty_batches():
     assert last.shape == ds0.shape == (0, 64) and not dv.any() and not dg.any()
 
 
+def _with_resets(dt):
+    """One sequence, cut into segments of several tiles: a strip of 64 channels that is reset every 97
+    tokens, one with a channel that forgets nothing, 8 channels with a reset in the middle of every other
+    segment or so."""
+    v, g, w, s0, _, rng = _case(17, 1, 44000, 136, dt, decay=0.02)
+    g[:, ::97, :64] = float("-inf")
+    g[:, :, 64:128] = -0.5
+    g[:, :, 70] = -1e-4
+    g[:, 300::1111, 128:] = -120.0
+    return v, g, w, s0, rng
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_long_sequences_with_resets(dt):
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, rng = _with_resets(dt)
+    do = draw(rng, *v.shape, dtype=DT[dt]).cuda()
+    say("linear_recurrence 44000 tokens with resets", dt)
+    o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
+    grads = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=s0)
+    cu = torch.tensor([0, 44000], dtype=torch.int32, device="cuda")
+    packed, plast = G.linear_recurrence_fwd(v, g, w, initial_state=s0, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    ref, bound, lref, lbound, m, e = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, DT[dt])
+    for x, y in ((o, last), (packed, plast)):
+        assert_within("o", x, ref, bound)
+        assert_within("last", y, lref, lbound)
+    kept = np.arange(64, 44000, 64)  # the states before these tokens, and before the first
+    assert_within("states", states.flatten()[:136].view(1, 136), f64(s0), 0 * f64(s0))
+    assert_within("states", states.flatten()[136:136 * (len(kept) + 1)].view(-1, 136), ref[0, kept - 1],
+                  e[0, kept - 1] + 2.0 ** -24 * np.abs(ref[0, kept - 1]) + 1e-38)
+    for x, (r, b) in zip(grads, recurrence_grad_bounds(f64(v), f64(g), f64(w), f64(do), f64(s0), f64(s0), None, DT[dt])):
+        assert_within("gradient", x, r, b)
+
+
+def test_states_that_are_not_finite_cross_resets():
+    """A NaN stays (0 NaN is NaN), an infinity until a decay of 0, in their channel, over all segments; the
+    other channels keep their values."""
+    import gated_delta_rule_36_amd as G
+    v, g, w, s0, _ = _with_resets("fp32")
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, torch.float32)
+    v[0, 1000, 3] = float("nan")
+    v[0, 20000, 131] = float("inf")
+    s0[0, 7] = float("-inf")  # meets a decay of 0 at the first token: NaN from there on
+    say("linear_recurrence NaN and infinity over resets")
+    o, last = G.linear_recurrence_fwd(v, g, w, initial_state=s0)
+    torch.cuda.synchronize()
+    bad = np.zeros((44000, 136), bool)
+    bad[1000:, 3] = bad[20000:, 131] = bad[:, 7] = True
+    got, end = f64(o)[0], f64(last)
+    assert np.isnan(got[1000:, 3]).all() and np.isnan(got[:, 7]).all() and not np.isfinite(got[20000:, 131]).any()
+    assert not np.isfinite(end[0, [3, 7, 131]]).any()
+    ok = ~bad[-1:]
+    assert (np.abs(got - ref[0])[~bad] <= bound[0][~bad]).all()
+    assert (np.abs(end - lref)[ok] <= lbound[ok]).all()
+
+
 def test_bad_values_stay_in_their_sequence_and_channel():
     import gated_delta_rule_36_amd as G
     v, g, w, s0, cu, rng = _case(10, 1, 0, 72, "bf16", lens=[70, 200, 0, 31])

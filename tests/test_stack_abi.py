@@ -64,8 +64,9 @@ def test_recurrence_workspace(what):
     sequences, short ones, none are not."""
     back = what == "bwd"
     ask = lambda *a: _lib.lib().gdn2_linear_recurrence_workspace_bytes(back, *a)  # noqa: E731
+    strip = 2 * 64 * 4 + 4  # a map and a count
     need = ask(0, 1, 5000, 64, 1)
-    assert need == 20 * 2 * 64 * 4  # 20 segments of 256 tokens
+    assert need == 20 * strip  # 20 segments of 256 tokens
     one = dict(B=1, N=1, T=5000)
     assert _rec(what, ws_=None, **one) == 3
     assert _rec(what, wsz=need - 1, **one) == 3
@@ -73,9 +74,11 @@ def test_recurrence_workspace(what):
     assert ask(0, 1, 300, 64, 1) == ask(0, 200, 5000, 64, 200) == ask(0, 1, 5000, 64, 2) == ask(0, 1, 5000, 60, 1) == 0
     assert (ask(0, 1, 700, 64, 1) > 0) == back        # backward from 384 tokens, forward from 768
     assert (ask(0, 140, 5000, 64, 140) > 0) == back   # and up to a larger part of the card
-    assert ask(1, 1, 5000, 64, 3) == (5000 // 256 + 3) * 2 * 64 * 4
+    assert ask(1, 1, 5000, 64, 3) == (5000 // 256 + 3) * strip
     # packed batches of many sequences: one of them may be much longer than the others
-    assert ask(1, 1, 200000, 64, 200) == (200000 // 1024 + 200) * 2 * 64 * 4
+    assert ask(1, 1, 200000, 64, 200) == (200000 // (1024 if back else 896) + 200) * strip
+    # a fair share of 256 workgroups forward, of 1024 backward
+    assert ask(0, 1, 200000, 64, 1) == (-(-200000 // (256 if back else 896))) * strip
     assert ask(0, 1, -1, 64, 1) == ask(0, 1, (1 << 31) - 1, 64, 1) == 0
 
 
