@@ -281,12 +281,14 @@ __device__ __forceinline__ void zero_outside(const RecurrenceArgs& a, T* x, cons
     if (t < first || t >= last) cn.template store<kSharedLines>(x + (long)t * a.D + strip, zero);
 }
 
-// How a cut forward runs: the first pass walks every segment from a zero state (the first segment from
-// the initial one), leaves the segment's map h -> A h + H, and writes the outputs from the tile on in
-// front of which the decay has taken everything of what came before (A = 0 in fp32 in all channels of the
-// strip); the second pass walks the tiles before that one again, from the state that the earlier maps
-// give. 32768 tokens of 2048 channels in bf16, in us (a pass for the maps alone and one for all outputs
-// takes 178 whatever the decays are):
+// How a cut forward runs. Short segments: a pass for the segments' maps h -> A h + H (below), then all
+// segments at once (kWhole), each from the state that the maps before it give. Long ones (see
+// recurrence_cut), which may forget what came before them: the first pass walks every segment from a zero
+// state (the first segment from the initial one), leaves its map, and writes the outputs from the tile on
+// in front of which the decay has taken everything of the state before (A = 0 in fp32 in all channels of
+// the strip); the second pass walks the tiles before that one again, from the state that the earlier
+// maps give. 32768 tokens of 2048 channels in bf16, in us (a pass for the maps and one for all outputs: 178
+// whatever the decays are):
 //   one token in 10 a reset to e^-5       132   (every tile of a segment but the first two is final)
 //   alpha 0.92 on average                 153
 //   nothing forgotten within a segment    183   (both passes read everything: 14 bytes an element)
@@ -339,18 +341,18 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   // The initial state goes through LDS from the lanes that write the final one, which may be the same
   // memory.
   float h = 0.f;
-  if (PASS != kSecond && p.index == 0 && a.s0 != nullptr) {
+  if (PASS != kSecond && (PASS == kWhole || p.index == 0) && a.s0 != nullptr) {
     if (wave == 0) s_map[1][0][0][own] = a.s0[(long)p.n * a.D + och];
     lds_barrier();
     h = s_map[1][0][0][own];
   }
   int parity = 0;
-  if constexpr (PASS == kSecond) {  // the maps of the segments before this one, the first of which starts from nothing
-    const int still = uniform(*opened);
+  if (PASS != kFirst && p.index > 0) {  // the maps of the segments before this one
+    const int still = PASS == kSecond ? uniform(*opened) : 0;
     fold_segments<false, NW>(a, unit - p.index, 0, p.index, strip, cn, lane, run, own, &s_map[0][0][0][0], h);
     parity = 1;
     // (a state that is not finite stays so, however far it decays)
-    if (__all(fabsf(h) < INFINITY) && still < p.end - p.begin) end = p.begin + still;
+    if (PASS == kSecond && __all(fabsf(h) < INFINITY) && still < p.end - p.begin) end = p.begin + still;
   }
   for (int t0 = p.begin; t0 < end; t0 += TILE) {
     const int mine = p.end - (t0 + run * R);  // tokens of this run, from R down to none
@@ -429,49 +431,57 @@ __global__ void __launch_bounds__(64 * NW) gdn2_recurrence_kernel(RecurrenceArgs
   }
 }
 
-// The maps e -> A e + L of the segments behind another, for the backward of long sequences. A lane walks
-// seg / 32 consecutive tokens of 8 channels, from the last to the first; the 32 runs are joined through
-// LDS.
-template <typename T>
+// The maps of the segments of long sequences, which run in parallel where sequences and channels
+// are too few to fill the card: forward h -> A h + H of every segment that another follows, backward
+// e -> A e + L of every segment behind another. A lane walks seg / 32 consecutive tokens of 8
+// channels; the 32 runs are joined through LDS.
+template <typename T, bool GATE, bool BACK>
 __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArgs a, const T* d_o) {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 4, NA = !BACK && GATE ? 3 : 2;
   __shared__ __attribute__((aligned(16))) float s_map[2][kRuns][kStrip];
   int unit, strip;
   if (!my_group(a, a.cut.units, unit, strip)) return;
   const Piece p = piece_of(a, unit);
-  if (p.begin >= p.end || p.begin == 0) return;
+  if (p.begin >= p.end || (BACK ? p.begin == 0 : p.end == p.len)) return;
   const int cg = threadIdx.x & 7, run = threadIdx.x >> 3;
   const Channels<T> cn(cg, strip, a.D);
-  const T* src[2] = {(const T*)a.g + p.first * a.g_stride + strip, d_o + p.first * a.D + strip};
-  const long stride[2] = {a.g_stride, (long)a.D};
+  const T* src[3] = {(const T*)a.g + strip, (BACK ? d_o : (const T*)a.v) + strip, GATE ? (const T*)a.w + strip : nullptr};
+  const long stride[3] = {a.g_stride, BACK ? (long)a.D : a.v_stride, a.w_stride};
   const int each = a.cut.seg / kRuns;
-  const int t0 = p.begin + run * each + each - 1;  // tokens t0, t0 - 1, .., those past the end counting as none
-  float G[8], L[8];
+  // tokens t0, t0 + 1, .. (BACK: t0, t0 - 1, ..), those past the end counting as none
+  const int t0 = p.begin + run * each + (BACK ? each - 1 : 0);
+  float G[8], H[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) G[c] = L[c] = 0.f;
-  auto load = [&](Raw<T, AHEAD, 2>& r, int i0) {
+  for (int c = 0; c < 8; ++c) G[c] = H[c] = 0.f;
+  auto load = [&](Raw<T, AHEAD, NA>& r, int i0) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const int t = t0 - i0 - i < p.end ? t0 - i0 - i : p.end - 1;
+      int t = BACK ? t0 - i0 - i : t0 + i0 + i;
+      t = t < p.end ? t : p.end - 1;
+      t = t > 0 ? t : 0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) cn.template load<kLines>(r.x[k][i], src[k] + t * stride[k]);
+      for (int k = 0; k < NA; ++k) cn.template load<kLines>(r.x[k][i], src[k] + (p.first + t) * stride[k]);
     }
   };
-  Raw<T, AHEAD, 2> cur, next;
+  Raw<T, AHEAD, NA> cur, next;
   load(cur, 0);
-  for (int i0 = 0; i0 < each; i0 += AHEAD) {  // (each is a multiple of AHEAD)
+  for (int i0 = 0; i0 < each; i0 += AHEAD) {
     if (i0 + AHEAD < each) load(next, i0 + AHEAD);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      float g[8], x[8];
+      const bool in = i0 + i < each && (BACK ? t0 - i0 - i : t0 + i0 + i) < p.end;
+      float g[8], x[8], w[8];
       cur.x[0][i].to_float(g);
       cur.x[1][i].to_float(x);
+      if constexpr (NA == 3) cur.x[2][i].to_float(w);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
+        if constexpr (NA == 3) x[c] *= w[c];
         g[c] *= kLog2e;
-        if (t0 - i0 - i >= p.end) g[c] = x[c] = 0.f;
+        if (!in) g[c] = x[c] = 0.f;
+        const float al = fast_exp2(g[c]);
         G[c] += g[c];
-        L[c] = fast_exp2(g[c]) * (x[c] + L[c]);
+        H[c] = BACK ? al * (x[c] + H[c]) : fmaf(al, H[c], x[c]);
       }
     }
     cur = next;
@@ -479,15 +489,16 @@ __global__ void __launch_bounds__(256) gdn2_recurrence_maps_kernel(RecurrenceArg
 #pragma unroll
   for (int c = 0; c < 8; ++c) G[c] = fast_exp2(G[c]);
   store8(&s_map[0][run][cg * 8], G);
-  store8(&s_map[1][run][cg * 8], L);
+  store8(&s_map[1][run][cg * 8], H);
   lds_barrier();
   if (threadIdx.x < kStrip) {
     const int c = strip + Channels<T>::place(threadIdx.x);
     float A = 1.f, B = 0.f;
 #pragma unroll 8
-    for (int k = kRuns - 1; k >= 0; --k) {
-      A *= s_map[0][k][threadIdx.x];
-      B = fmaf(s_map[0][k][threadIdx.x], B, s_map[1][k][threadIdx.x]);
+    for (int k = 0; k < kRuns; ++k) {
+      const int r = BACK ? kRuns - 1 - k : k;
+      A *= s_map[0][r][threadIdx.x];
+      B = fmaf(s_map[0][r][threadIdx.x], B, s_map[1][r][threadIdx.x]);
     }
     if (c < a.D) {
       a.cut.maps[(long)unit * 2 * a.D + c] = A;
@@ -706,13 +717,16 @@ long recurrence_state_slots(bool packed, int B, int T, int N) {
 // is forgotten) and backward in us:
 //   sequences                 1          2          3          4          5
 //   uncut                 69, 140    69, 141    72, 146    77, 150    86, 158
-//   cut                   27,  31    45,  60    64,  91    85, 113   119, 150
+//   cut                   24,  31    43,  60    64,  91    85, 113   119, 150
 // and of 6 the backward 170 uncut, 175 cut. Where workgroups run past a whole round of the card (9
 // sequences, 288: 80 and 145 uncut, 84 and 120 cut) the last round counts like a full one: cut where less
-// than 0.44 (0.66) of the rounds is used. The units fill the card: forward with one workgroup of 8 waves a
-// compute unit, since a longer segment has a larger part behind what it forgets (1 x 32768 at 256, 512 and
-// 1024 workgroups 152, 179 and 195), backward with four of 4. Packed batches, whose lengths the host does not
-// know, are cut at least into units of a 256th in any case, for a sequence much longer than the others.
+// than 0.44 (0.66) of the rounds is used. Units fill the card with four workgroups of 4 waves a compute
+// unit. A forward whose fair share of one workgroup of 8 waves a compute unit is 1024 tokens or more takes
+// that, and two passes of the outputs (see above; with resets, without, nothing forgotten, against a pass for
+// the maps: segments of 512 tokens, 1 x 4096, 24, 27, 28 against 24; of 1024, 2 x 4096, 34, 45, 45 against 43;
+// of 1536, 3 x 4096, 57, 64, 64 against 67; of 2048, 1 x 16384, 69, 83, 92 against 86). Packed batches, whose
+// lengths the host does not know, are cut at four times the fair share in any case, for a sequence much
+// longer than the others.
 RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, int N) {
   constexpr int TILE = 128;
   RecurrenceCut c{};
@@ -721,14 +735,13 @@ RecurrenceCut recurrence_cut(bool backward, bool packed, int B, int T, int D, in
   c.per_sequence = 1;
   c.units = N;
   if (T < (backward ? 3 : 6) * TILE || N == 0 || N > kMaxGroups) return c;
-  const long share = backward ? 1024 : 256;
-  long seg = ((tokens * strips + share - 1) / share + TILE - 1) / TILE * TILE;  // the fair share
-  if (seg < 2 * TILE) seg = 2 * TILE;
   const long rounds = (groups + 255) / 256;
-  if (groups * 100 >= rounds * 256 * (backward ? 66 : 44)) {
-    if (!packed) return c;
-    seg *= share / 256;
-  }
+  const bool few = groups * 100 < rounds * 256 * (backward ? 66 : 44);
+  if (!few && !packed) return c;
+  const auto share = [&](long of) { return ((tokens * strips + of - 1) / of + TILE - 1) / TILE * TILE; };
+  c.twice = !backward && few && share(256) >= 1024;
+  long seg = share(c.twice || !few ? 256 : 1024);
+  if (seg < 2 * TILE) seg = 2 * TILE;
   if (seg >= T) return c;
   c.cut = true;
   c.seg = (int)seg;
@@ -755,8 +768,8 @@ bool at_lines(const void* p, long stride, size_t size) {
 // Inputs of more than half the Infinity Cache (256 MB) are read past the caches: 8 x 2048 tokens of
 // 2048 channels in bf16 60 -> 57 us; of half as many, where repeated calls find them there, 26 -> 30.
 // (Rows that share lines lose by it: 7 packed sequences of 520 channels in fp32 29 -> 37, and their
-// backward by stores past the caches, 8 x 1024 x 1000 in bf16 42 -> 51.) A cut forward, which reads them
-// twice, does so from the whole cache on: 16384 tokens of 2048 channels 73 -> 69.
+// backward by stores past the caches, 8 x 1024 x 1000 in bf16 42 -> 51.) A forward in two passes,
+// which reads them twice, does so from the whole cache on: 16384 tokens of 2048 channels 73 -> 69.
 bool streamed(const RecurrenceArgs& a, long tokens, int arrays, size_t size, long limit = 128) {
   return tokens * a.D * arrays * (long)size > limit << 20;
 }
@@ -769,7 +782,7 @@ template <typename T, bool GATE, int MODE>
 void launch_forward(const RecurrenceArgs& a) {
   const hipStream_t st = (hipStream_t)a.stream;
   const dim3 grid(grid_of(a, a.cut.units + a.zero_rest));
-  if (a.cut.cut) {  // what the first pass reads through the caches, the second finds there in part
+  if (a.cut.cut && a.cut.twice) {  // what the first pass reads through the caches, the second finds there in part
     constexpr int FIRST = MODE == kStream ? kLines : MODE;
     hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, FIRST, kFirst>), grid, dim3(512), 0, st, a);
     hipLaunchKernelGGL((gdn2_recurrence_kernel<T, GATE, 8, MODE, kSecond>), dim3(grid_of(a, a.cut.units)), dim3(512), 0, st, a);
@@ -785,8 +798,11 @@ hipError_t forward(RecurrenceArgs a) {
   a.zero_rest = a.cu_seqlens != nullptr && a.states != nullptr && a.o != nullptr;
   a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
                    !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(a.o, a.D, sizeof(T));
+  if (a.cut.cut && !a.cut.twice)
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, GATE, false>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
+                       (hipStream_t)a.stream, a, (const T*)nullptr);
   if (a.shared_lines) launch_forward<T, GATE, kSharedLines>(a);
-  else if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T), a.cut.cut ? 256 : 128)) launch_forward<T, GATE, kStream>(a);
+  else if (streamed(a, tokens, GATE ? 3 : 2, sizeof(T), a.cut.cut && a.cut.twice ? 256 : 128)) launch_forward<T, GATE, kStream>(a);
   else launch_forward<T, GATE, kLines>(a);
   return hipGetLastError();
 }
@@ -811,7 +827,7 @@ hipError_t backward(RecurrenceBwdArgs b) {
   a.shared_lines = !at_lines(a.v, a.v_stride, sizeof(T)) || !at_lines(a.g, a.g_stride, sizeof(T)) ||
                    !at_lines(a.w, a.w_stride, sizeof(T)) || !at_lines(b.d_o, a.D, sizeof(T));
   if (a.cut.cut)
-    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
+    hipLaunchKernelGGL((gdn2_recurrence_maps_kernel<T, false, true>), dim3(grid_of(a, a.cut.units)), dim3(256), 0,
                        (hipStream_t)a.stream, a, (const T*)b.d_o);
   if (a.shared_lines) launch_backward<T, GATE, kSharedLines>(b);
   else if (streamed(a, tokens, GATE ? 4 : 3, sizeof(T))) launch_backward<T, GATE, kStream>(b);

@@ -102,6 +102,9 @@ int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
   gdn2::RecurrenceArgs a = recurrence_args(false, v, log_alpha, w, cu_seqlens, B, T, D, N, v_stride,
                                            g_stride, w_stride, dtype, workspace, hip_stream);
   a.s0 = initial_state; a.o = o; a.sN = final_state; a.states = states;
+  // (of two passes only the first reads the initial states, and a sequence of several units gets its final
+  // one in the second)
+  if (final_state != nullptr && final_state == initial_state) a.cut.twice = true;
   return status_of(gdn2::launch_recurrence(a));
 }
 

@@ -19,7 +19,8 @@ struct RecurrenceCut {
   int seg;           // tokens of a unit
   int per_sequence;  // units of a sequence (packed batches: see the kernels)
   int units;
-  float* maps;       // workspace, where cut: [units, 2, D], then int [units, strips]
+  bool twice;        // forward: two passes of the outputs, none for the maps alone
+  float* maps;       // workspace, where cut: [units, 2, D], then int [units, strips] (for `twice`)
 };
 struct RecurrenceArgs {
   const void *v, *g, *w;      // [tokens, D], rows dense, one stride each; w may be null (ones)

@@ -191,7 +191,7 @@ def _with_resets(dt):
     """One sequence, cut into segments of several tiles: a strip of 64 channels that is reset every 97
     tokens, one with a channel that forgets nothing, 8 channels with a reset in the middle of every other
     segment or so."""
-    v, g, w, s0, _, rng = _case(17, 1, 44000, 136, dt, decay=0.02)
+    v, g, w, s0, _, rng = _case(17, 1, 80000, 136, dt, decay=0.02)
     g[:, ::97, :64] = float("-inf")
     g[:, :, 64:128] = -0.5
     g[:, :, 70] = -1e-4
@@ -204,17 +204,17 @@ def test_long_sequences_with_resets(dt):
     import gated_delta_rule_36_amd as G
     v, g, w, s0, rng = _with_resets(dt)
     do = draw(rng, *v.shape, dtype=DT[dt]).cuda()
-    say("linear_recurrence 44000 tokens with resets", dt)
+    say("linear_recurrence 80000 tokens with resets", dt)
     o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
     grads = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=s0)
-    cu = torch.tensor([0, 44000], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 80000], dtype=torch.int32, device="cuda")
     packed, plast = G.linear_recurrence_fwd(v, g, w, initial_state=s0, cu_seqlens=cu)
     torch.cuda.synchronize()
     ref, bound, lref, lbound, m, e = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, DT[dt])
     for x, y in ((o, last), (packed, plast)):
         assert_within("o", x, ref, bound)
         assert_within("last", y, lref, lbound)
-    kept = np.arange(64, 44000, 64)  # the states before these tokens, and before the first
+    kept = np.arange(64, 80000, 64)  # the states before these tokens, and before the first
     assert_within("states", states.flatten()[:136].view(1, 136), f64(s0), 0 * f64(s0))
     assert_within("states", states.flatten()[136:136 * (len(kept) + 1)].view(-1, 136), ref[0, kept - 1],
                   e[0, kept - 1] + 2.0 ** -24 * np.abs(ref[0, kept - 1]) + 1e-38)
@@ -234,7 +234,7 @@ def test_states_that_are_not_finite_cross_resets():
     say("linear_recurrence NaN and infinity over resets")
     o, last = G.linear_recurrence_fwd(v, g, w, initial_state=s0)
     torch.cuda.synchronize()
-    bad = np.zeros((44000, 136), bool)
+    bad = np.zeros((80000, 136), bool)
     bad[1000:, 3] = bad[20000:, 131] = bad[:, 7] = True
     got, end = f64(o)[0], f64(last)
     assert np.isnan(got[1000:, 3]).all() and np.isnan(got[:, 7]).all() and not np.isfinite(got[20000:, 131]).any()
@@ -288,6 +288,24 @@ def test_final_state_in_place_and_repeatable():
                 s.data_ptr(), None, None, 5, 333, 264, 5, 264, 264, 264, 0, None, 0)
     torch.cuda.synchronize()
     assert torch.equal(s, runs[0][1]) and torch.equal(o, runs[0][0])
+
+
+@pytest.mark.parametrize("B,T", [(1, 9000), (3, 2000)])
+def test_final_state_in_place_of_cut_sequences(B, T):
+    import gated_delta_rule_36_amd as G
+    from gated_delta_rule_36_amd import _attn, _lib
+    v, g, w, s0, _, _ = _case(18, B, T, 72, "fp32", decay=0.001)
+    need = int(_lib.lib().gdn2_linear_recurrence_workspace_bytes(0, 0, B, T, 72, B))
+    assert need > 0
+    say("linear_recurrence in place, cut", B, T)
+    s, o = s0.clone(), torch.empty_like(v)
+    ws = torch.empty(need // 4, device="cuda")
+    _attn._call("gdn2_linear_recurrence", v.device, v.data_ptr(), g.data_ptr(), w.data_ptr(), s.data_ptr(), o.data_ptr(),
+                s.data_ptr(), None, None, B, T, 72, B, 72, 72, 72, 1, ws.data_ptr(), need)
+    torch.cuda.synchronize()
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(f64(v), f64(g), f64(w), f64(s0), None, torch.float32)
+    assert_within("o", o, ref, bound)
+    assert_within("last", s, lref, lbound)
 
 
 def test_long_memory():
@@ -416,3 +434,36 @@ def test_capture_replay_and_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, ref))
+
+
+def test_cut_sequences_in_two_graphs():
+    """Two captured calls of cut sequences, replayed in turn and at the same time on two streams, each
+    with a workspace of its own."""
+    import gated_delta_rule_36_amd as G
+    sides = []
+    for seed in (21, 22):
+        v, g, w, s0, _, rng = _case(seed, 1, 9000, 72, "bf16", decay=0.05)
+        do = draw(rng, *v.shape).cuda()
+
+        def all_of(v=v, g=g, w=w, s0=s0, do=do):
+            o, last, states = G.linear_recurrence_fwd_train(v, g, w, initial_state=s0)
+            return (o, last, *G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=last))
+
+        say("linear_recurrence cut, captured", seed)
+        all_of()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = all_of()
+        sides.append((graph, held, all_of, v, torch.cuda.Stream()))
+    for seed in range(3):
+        for graph, held, all_of, v, stream in sides:
+            v.copy_(draw(np.random.default_rng(seed), *v.shape))
+        torch.cuda.synchronize()
+        for graph, _, _, _, stream in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, held, all_of, _, _ in sides:
+            assert all(torch.equal(a, b) for a, b in zip(held, all_of()))
+        torch.cuda.synchronize()

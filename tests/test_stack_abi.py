@@ -76,9 +76,10 @@ def test_recurrence_workspace(what):
     assert (ask(0, 140, 5000, 64, 140) > 0) == back   # and up to a larger part of the card
     assert ask(1, 1, 5000, 64, 3) == (5000 // 256 + 3) * strip
     # packed batches of many sequences: one of them may be much longer than the others
-    assert ask(1, 1, 200000, 64, 200) == (200000 // (1024 if back else 896) + 200) * strip
-    # a fair share of 256 workgroups forward, of 1024 backward
-    assert ask(0, 1, 200000, 64, 1) == (-(-200000 // (256 if back else 896))) * strip
+    assert ask(1, 1, 200000, 64, 200) == (200000 // 896 + 200) * strip
+    # a fair share of 1024 workgroups; forward, where that of 256 is 1024 tokens or more, of 256
+    assert ask(0, 1, 200000, 64, 1) == -(-200000 // 256) * strip
+    assert ask(0, 1, 300000, 64, 1) == -(-300000 // (384 if back else 1280)) * strip
     assert ask(0, 1, -1, 64, 1) == ask(0, 1, (1 << 31) - 1, 64, 1) == 0
 
 
