@@ -274,10 +274,14 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
     for (int e = 0; e < E; ++e) store8(&s_part[mine][(e * LANES + in_row) * 8], dw[e]);
     __syncthreads();
     for (int ch = threadIdx.x * 4; ch < a.D; ch += 1024) {
-      f4 s = *reinterpret_cast<const f4*>(&s_part[0][ch]);
+      double s[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int u = 1; u < ROWS; ++u) s += *reinterpret_cast<const f4*>(&s_part[u][ch]);
-      *reinterpret_cast<f4*>(out + ch) = s;
+      for (int u = 0; u < ROWS; ++u) {
+        const f4 x = *reinterpret_cast<const f4*>(&s_part[u][ch]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[c] += x[c];
+      }
+      *reinterpret_cast<f4*>(out + ch) = f4{(float)s[0], (float)s[1], (float)s[2], (float)s[3]};
     }
   } else {
 #pragma unroll
@@ -289,11 +293,12 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
 }
 
 // The weight's gradient: 32 channels (a line of the partial sums) a workgroup, 32 of its lanes walking
-// the sums of each.
+// the sums of each. What several rows' lanes leave is added in fp64, at no cost in time (22684 rows of 64
+// channels in fp32: 0.8e-7 off the formula in the 2-norm, 2.0e-7 with all sums in fp32).
 __global__ void __launch_bounds__(1024) gdn2_residual_norm_dweight_kernel(const float* partial, float* dweight, int D, int groups) {
-  __shared__ float s[32][32];
+  __shared__ double s[32][32];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5, ch = blockIdx.x * 32 + c;
-  float x = 0.f;
+  double x = 0;
   if (ch < D) {
 #pragma unroll 16
     for (int g = k; g < groups; g += 32) x += partial[(long)g * D + ch];
@@ -301,10 +306,10 @@ __global__ void __launch_bounds__(1024) gdn2_residual_norm_dweight_kernel(const 
   s[k][c] = x;
   __syncthreads();
   if (k == 0 && ch < D) {
-    float t = 0.f;
+    double t = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) t += s[i][c];
-    dweight[ch] = t;
+    dweight[ch] = (float)t;
   }
 }
 
