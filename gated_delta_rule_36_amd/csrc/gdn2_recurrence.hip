@@ -7,10 +7,12 @@
 // (A2 A1, A2 B1 + B2). The kernels are bound by HBM (4 flops an element forward, 8 bytes in bf16),
 // so each input is read once and a sequence's state stays on the chip: one workgroup owns 64
 // channels of a sequence (a row of them is one 128-byte line in bf16) and walks it in tiles of
-// 32 runs of R tokens. A lane holds one run of 8 channels; the runs' maps are scanned across a
-// wave's 8 runs by register exchanges and across the 4 waves through LDS, one barrier a tile,
+// 32 or 64 runs of R tokens. A lane holds one run of 8 channels; the runs' maps are scanned across a
+// wave's 8 runs by register exchanges and across the 4 or 8 waves through LDS, one barrier a tile,
 // while the next tile's loads are in flight. A run's outputs are then the recurrence itself, from
-// the state that enters it.
+// the state that enters it. 8 x 2048 tokens of 2048 channels in bf16: 57 us forward (4.7 TB/s), 102
+// backward (4.6), where a copy moves 5.4 TB/s and inputs at a stride of 4224 bytes run 50 forward.
+// Long sequences of few channels are cut into segments (see below), whose inputs are read again.
 //
 // Precision: fp32. A run's decay is exp of the sum of its logarithms, so that a state that lives
 // for thousands of tokens takes one rounding of its decay per run and not per token.
@@ -24,7 +26,7 @@ namespace gdn2 {
 namespace {
 
 constexpr int kStrip = 64;   // channels of a workgroup
-constexpr int kRuns = 32;    // runs of 4 waves
+constexpr int kRuns = 32;    // runs of 4 waves (of the maps' pass)
 
 __host__ __device__ constexpr int strips_of(int D) { return (D + kStrip - 1) / kStrip; }
 

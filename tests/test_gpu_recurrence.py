@@ -70,6 +70,9 @@ CASES = [
     (1, 0, 64, "bf16", True, True, [256, 0, 1025, 1, 512, 257], False, 0.01, 0),
     (1, 0, 136, "fp32", True, True, [3000, 0, 7], True, 0.01, 300),
     (1, 0, 8, "fp32", True, True, [3, 9000] + 80 * [7], False, 0.01, 0),
+    # the same, in segments long enough to forget what came before them, rows in whole lines
+    (1, 8192, 2048, "bf16", True, True, None, False, 0.3, 0),
+    (1, 0, 2048, "fp32", False, True, [20, 5000, 3200], False, 0.3, 0),
     # not cut for its many groups, and past the eight-wave form
     (1, 0, 8, "bf16", True, True, 600 * [2, 0, 1], False, 0.1, 0),
     (130, 400, 8, "bf16", True, False, None, False, 0.1, 0),
