@@ -247,3 +247,29 @@ def test_capture_and_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, ref))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows, which alone have a gradient."""
+    import gated_delta_rule_36_amd as G
+    rows, D, n = 530000, 4096, 50
+    say("residual_norm offsets past 32 bits")
+    torch.manual_seed(5)
+    x, r = (torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    w = 1 + 0.3 * torch.randn(D, device="cuda")
+    y, h = G.residual_norm_fwd(x, r, w)
+    codes, scale, h8 = G.residual_norm_8bit(x, r, w, group=32)
+    dy = torch.zeros_like(x)
+    dy[-n:].normal_()
+    dx, dr, dw = G.residual_norm_bwd(dy, None, h, w)
+    torch.cuda.synchronize()
+    ref = _stream(x[-n:], r[-n:])
+    assert torch.equal(h[-n:].cpu(), ref) and torch.equal(h8[-n:].cpu(), ref)
+    assert_within("y", y[-n:], *norm_bound(f64(ref), f64(w), 1e-6, x.dtype))
+    _, s, _ = R.norm_8bit(f64(ref), f64(w), 1e-6, 32)
+    assert np.array_equal(f64(scale[-n:]), s)
+    small = G.residual_norm_8bit(x[-n:], r[-n:], w, group=32)[0]
+    assert torch.equal(codes[-n:].view(torch.uint8), small.view(torch.uint8))
+    gx, bx, _, rw, bw = norm_grad_bounds(f64(dy[-n:]), None, f64(ref), f64(w), 1e-6, x.dtype, x.dtype)
+    assert_within("dx", dx[-n:], gx, bx)
+    assert_within("dweight", dw, rw, bw)

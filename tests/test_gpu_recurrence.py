@@ -470,3 +470,25 @@ def test_cut_sequences_in_two_graphs():
         for _, held, all_of, _, _ in sides:
             assert all(torch.equal(a, b) for a, b in zip(held, all_of()))
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("B,T", [(1, 540000), (132, 4096)])
+def test_offsets_past_32_bits(B, T):
+    """More than 2^31 elements, cut and not: the last tokens of the last sequence, behind a reset."""
+    import gated_delta_rule_36_amd as G
+    D, n = 4096, 700
+    say("linear_recurrence offsets past 32 bits", B, T)
+    torch.manual_seed(B)
+    v, g, w, do = (torch.empty(B, T, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(4))
+    g.abs_().mul_(-0.1)
+    g[-1, -n] = float("-inf")
+    ds = torch.randn(B, D, device="cuda")
+    o, last, states = G.linear_recurrence_fwd_train(v, g, w)
+    grads = G.linear_recurrence_bwd(v, g, w, states, do, d_final_state=ds)
+    torch.cuda.synchronize()
+    tail = [f64(t[-1:, -n:]) for t in (v, g, w, do)]
+    ref, bound, lref, lbound, _, _ = recurrence_bounds(*tail[:3], None, None, torch.bfloat16)
+    assert_within("o", o[-1:, -n:], ref, bound)
+    assert_within("last", last[-1:], lref, lbound)
+    for x, (r, b) in zip(grads[:3], recurrence_grad_bounds(*tail, None, f64(ds[-1:]), None, torch.bfloat16)):
+        assert_within("gradient", x[-1:, -n:], r, b)

@@ -162,3 +162,21 @@ def test_workspace_stream_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(held[0], ref[0]) and torch.equal(held[1], ref[1])
+
+
+def test_offsets_past_32_bits():
+    """The widest vocabulary, 2^31 probabilities: a draft accepted and one rejected at the rows' ends; a
+    sequence without drafts."""
+    import gated_delta_rule_36_amd as G
+    N, L, V = 2, 3, 1 << 28
+    say("verify_drafts offsets past 32 bits")
+    p, q = torch.zeros(N, L + 1, V, device="cuda"), torch.zeros(N, L, V, device="cuda")
+    p[0, 0, V - 1] = 1
+    p[1, 0, V - 3], q[1, 0, V - 3] = 0.5, 0.25
+    p[1, 1, V - 5], p[1, 1, V - 2], q[1, 1, V - 5] = 0.6, 0.4, 0.6
+    drafts = torch.tensor([[0, 0, 0], [V - 3, 7, 0]], dtype=torch.int32, device="cuda")
+    u = torch.full((N, L + 1), 0.9, device="cuda")
+    lens = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    tokens, commit = G.verify_drafts(p, drafts, u, draft_probs=q, draft_len=lens)
+    torch.cuda.synchronize()
+    assert tokens.tolist() == [[V - 1, -1, -1, -1], [V - 3, V - 2, -1, -1]] and commit.tolist() == [1, 2]
