@@ -100,8 +100,7 @@ def _recurrence_sizes(backward, packed, B, T, D, N):
 
 
 def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
-    sizes = _recurrence_args(v, g, w, cu_seqlens)
-    B, T, D, N, strides, code, dev, dt = sizes
+    B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
     if initial_state is not None:
         _dense("initial_state", initial_state, (N, D), torch.float32, dev)
     o = _empty(v)
@@ -111,7 +110,7 @@ def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
     ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence", dev, v.data_ptr(), g.data_ptr(), _p(w), _p(initial_state),
           o.data_ptr(), _p(last), _p(states), _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
-    return o, last, states, sizes
+    return o, last, states
 
 
 def linear_recurrence_fwd(v, g, w=None, initial_state=None, cu_seqlens=None,
@@ -134,7 +133,7 @@ def linear_recurrence_fwd_train(v, g, w=None, initial_state=None, cu_seqlens=Non
     """linear_recurrence_fwd for training: (o, final_state, states), the last for
     linear_recurrence_bwd (the fp32 state before every 64th token of every sequence). Rows that belong
     to no packed sequence are zeros."""
-    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)[:3]
+    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)
 
 
 def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=None):
@@ -154,7 +153,7 @@ def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=No
 
 
 def _recurrence_bwd(v, g, w, states, do, d_final_state, cu_seqlens, sizes):
-    """The call itself, of checked tensors (autograd's are the forward's own)."""
+    """The call itself, of checked tensors."""
     B, T, D, N, strides, code, dev, dt = sizes
     need = _recurrence_sizes(True, cu_seqlens is not None, B, T, D, N)[0]
     dv, dg = torch.empty_like(do), torch.empty_like(do)
@@ -170,7 +169,7 @@ def _recurrence_bwd(v, g, w, states, do, d_final_state, cu_seqlens, sizes):
 class _LinearRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, v, g, w, initial_state, cu_seqlens):
-        o, last, states, ctx.sizes = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
+        o, last, states = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
         ctx.set_materialize_grads(False)
         ctx.has_s0 = initial_state is not None
         ctx.save_for_backward(v, g, w, states, cu_seqlens)
@@ -179,10 +178,10 @@ class _LinearRecurrence(torch.autograd.Function):
     @staticmethod
     @_no_second
     def backward(ctx, do, d_last):
-        v, g, w, states, cu = ctx.saved_tensors
+        v, g, w, states, cu = ctx.saved_tensors  # under hooks other tensors than the forward's: checked again
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _aligned_gradient(do)
         d_last = None if d_last is None else _aligned_gradient(d_last)
-        dv, dg, dw, ds0 = _recurrence_bwd(v, g, w, states, do, d_last, cu, ctx.sizes)
+        dv, dg, dw, ds0 = linear_recurrence_bwd(v, g, w, states, do, d_last, cu)
         return dv, dg, dw, ds0 if ctx.has_s0 else None, None
 
 

@@ -1,0 +1,48 @@
+"""GPU tests of training with the saved tensors moved away and back (activation offload)."""
+import pytest
+import torch
+
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _on_host():
+    return torch.autograd.graph.save_on_cpu()
+
+
+def _dense_copies():
+    return torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t)
+
+
+@pytest.mark.parametrize("hooks", [_on_host, _dense_copies])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,D,lens", [(70, 40, None), (3000, 64, None), (300, 72, [100, 0, 150])])
+def test_recurrence_on_slices(hooks, dt, T, D, lens):
+    """Slices of one projection come back dense: the gradients are those without hooks, bit for bit."""
+    import gated_delta_rule_36_amd as G
+    torch.manual_seed(T)
+    x = torch.randn(1, T, 3 * D + 8, device="cuda", dtype=dt)
+    x[..., D:2 * D] = -0.1 * x[..., D:2 * D].abs()
+    x.requires_grad_()
+    cu = None if lens is None else torch.tensor([0, *torch.tensor(lens).cumsum(0)], dtype=torch.int32, device="cuda")
+    s0 = torch.randn(1 if lens is None else len(lens), D, device="cuda").requires_grad_()
+    do, ds = torch.randn(1, T, D, device="cuda", dtype=dt), torch.randn_like(s0)
+    say("linear_recurrence under saved-tensor hooks", hooks.__name__, dt, T, D, lens)
+
+    def step():
+        out = G.linear_recurrence(*(x[..., k * D:(k + 1) * D] for k in range(3)), initial_state=s0, cu_seqlens=cu)
+        return out, torch.autograd.grad(out, (x, s0), (do, ds), retain_graph=True)
+
+    plain, ref = step()
+    with hooks():
+        out, got = step()
+    torch.cuda.synchronize()
+    for a, b in zip((*plain, *ref), (*out, *got)):
+        assert torch.equal(a, b)
