@@ -328,7 +328,7 @@ def residual_norm_bwd(dy, dh, h, weight, eps=1e-6):
 
 
 def _norm_bwd(dy, dh, h, weight, eps):
-    """The call itself, of checked tensors (autograd's are the forward's own)."""
+    """The call itself, of checked tensors."""
     D = weight.numel()
     rows, code, hcode = dy.numel() // D, _CODES[dy.dtype], _CODES[h.dtype]
     dx = torch.empty_like(dy)
@@ -355,10 +355,10 @@ class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     @_no_second
     def backward(ctx, dy, dh=None):
-        h, weight = ctx.saved_tensors
+        h, weight = ctx.saved_tensors  # under hooks other tensors than the forward's: checked again
         dy = torch.zeros(h.shape, dtype=ctx.dt, device=h.device) if dy is None else _aligned_gradient(dy)
         dh = None if dh is None else _aligned_gradient(dh)
-        dx, dr, dw = _norm_bwd(dy, dh, h, weight, ctx.eps)
+        dx, dr, dw = residual_norm_bwd(dy, dh, h, weight, ctx.eps)
         return dx, dr if ctx.needs_input_grad[1] else None, dw, None
 
 

@@ -46,3 +46,26 @@ def test_recurrence_on_slices(hooks, dt, T, D, lens):
     torch.cuda.synchronize()
     for a, b in zip((*plain, *ref), (*out, *got)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("hooks", [_on_host, _dense_copies])
+@pytest.mark.parametrize("dt,rt", [(torch.bfloat16, torch.float32), (torch.bfloat16, None), (torch.float32, torch.float32)])
+def test_norm_on_slices(hooks, dt, rt):
+    import gated_delta_rule_36_amd as G
+    torch.manual_seed(4)
+    x = torch.randn(50, 96 + 8, device="cuda", dtype=dt).requires_grad_()
+    r = None if rt is None else torch.randn(50, 96, device="cuda", dtype=rt).requires_grad_()
+    w = (1 + 0.3 * torch.randn(96, device="cuda")).requires_grad_()
+    dy, dh = torch.randn(50, 96, device="cuda", dtype=dt), torch.randn(50, 96, device="cuda", dtype=rt or dt)
+    say("residual_norm under saved-tensor hooks", hooks.__name__, dt, rt)
+
+    def step():
+        out = G.residual_norm(x[:, :96], r, w)
+        return out, torch.autograd.grad(out, [t for t in (x, r, w) if t is not None], (dy, dh), retain_graph=True)
+
+    plain, ref = step()
+    with hooks():
+        out, got = step()
+    torch.cuda.synchronize()
+    for a, b in zip((*plain, *ref), (*out, *got)):
+        assert torch.equal(a, b)

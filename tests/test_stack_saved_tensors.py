@@ -1,4 +1,4 @@
-"""Saved-tensor hooks around the recurrence's autograd on the host (the entry points replaced): what the
+"""Saved-tensor hooks around the autograd of the recurrence and the norm on the host (the entry points replaced): what the
 hooks hand back need not have the layout, nor the type, of what was saved."""
 import pytest
 import torch
@@ -63,3 +63,31 @@ def test_recurrence_refuses_other_tensors_than_it_saved(calls, change, dims):
     with pytest.raises((TypeError, ValueError)):
         o.sum().backward()
     assert len(calls) == made
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("change", [lambda t: t.double(), lambda t: t.float() if t.dtype == torch.bfloat16 else t.bfloat16(),
+                                    lambda t: t[..., :8], lambda t: t[:1], lambda t: t.to("meta")])
+@pytest.mark.parametrize("dims", [1, 2])
+def test_norm_refuses_other_tensors_than_it_saved(calls, change, dims, wide):
+    """The stream (2 axes) or the weight (1) in another type or shape, or on another device: the gradients
+    are of the saved ones."""
+    import gated_delta_rule_36_amd as G
+    x = torch.zeros(3, 16, dtype=torch.bfloat16)
+    r = torch.zeros(3, 16, dtype=torch.float32 if wide else torch.bfloat16, requires_grad=True)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: change(t) if t.dim() == dims else t):
+        y, h = G.residual_norm(x, r, torch.ones(16))
+    made = len(calls)
+    with pytest.raises((TypeError, ValueError)):
+        torch.autograd.backward((y, h), (torch.zeros_like(y), torch.zeros_like(h)))
+    assert len(calls) == made
+
+
+def test_norm_reads_the_unpacked_stream_at_its_stride(calls):
+    import gated_delta_rule_36_amd as G
+    x = torch.zeros(3, 40).requires_grad_()
+    with torch.autograd.graph.saved_tensors_hooks(_dense_copy, lambda t: t):
+        y, _ = G.residual_norm(x[:, :16], None, torch.ones(16))
+    y.sum().backward()
+    name, a = calls[-1]
+    assert name == "gdn2_residual_norm_bwd" and a[7:10] == (3, 16, 16)
