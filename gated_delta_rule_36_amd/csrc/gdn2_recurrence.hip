@@ -710,7 +710,9 @@ __global__ void __launch_bounds__(64) gdn2_recurrence_tokens_kernel(RecurrenceTo
 }
 
 long recurrence_state_slots(bool packed, int B, int T, int N) {
-  return packed ? (long)T / kStateTokens + N : (long)B * ((T + kStateTokens - 1) / kStateTokens);
+  if (!packed) return (long)B * ((T + kStateTokens - 1) / kStateTokens);
+  const long slots = (long)T / kStateTokens + N;
+  return slots == 0 && T > 0 ? 1 : slots;  // rows without sequences: the states' pointer says that this is training
 }
 
 // A unit takes a workgroup for each of its strips. Uncut, units are sequences: with few of them most of

@@ -55,7 +55,8 @@ struct RecurrenceTokensArgs {
 };
 
 // Kept states: one before every kStateTokens tokens of a sequence. Sequence n's begin at slot
-// n * ceil(T / kStateTokens), packed at cu_seqlens[n] / kStateTokens + n.
+// n * ceil(T / kStateTokens), packed at cu_seqlens[n] / kStateTokens + n. (Where there are tokens there is
+// a slot: the pointer is never null.)
 constexpr int kStateTokens = 64;
 constexpr int kMaxStride = 1 << 21;  // elements from one token to the next
 long recurrence_state_slots(bool packed, int B, int T, int N);

@@ -532,7 +532,7 @@ size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, in
  *   (With `states`, for training, rows that belong to no packed sequence are written as zeros.)
  *   Supported: D a multiple of 8, both dtypes, B * T below 2^31 - 4096, N * D / 64 below 2^23 (D
  *   rounded up to 64). A NaN or an infinity stays in its own sequence and
- *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 is a no-op.
+ *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 without `states` is a no-op.
  * Returns GDN2_OK or an error status.
  */
 int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
