@@ -6,9 +6,9 @@
 // u = dy weight and n = h rho:
 //     dh_total = dh + rho (u - n mean(u n)) = dx = dr,   dweight = sum over rows of dy n.
 //
-// Bound by HBM: every row is read once and kept in registers between the sum and the output.
-
-#include <type_traits>
+// Bound by HBM: every row is read once and kept in registers between the sum and the output. Sums over a
+// row are in fp64, whose exponent holds the square of any fp32 value and the product of any two; rho and
+// mean(u n) are back in fp32's range where the row's root mean square is.
 
 #include "gdn2_attn_device.h"
 #include "gdn2_stack_device.h"
@@ -47,6 +47,13 @@ __device__ __forceinline__ void row_total(T (&x)[K], T (*s)[W], int wave) {
   }
 }
 
+// 1 / sqrt(x) to fp32's precision of an x whose exponent may lie far outside fp32's (four powers of two at a
+// time into 0.5 .. 2, and back).
+__device__ __forceinline__ float rsqrt_of(double x) {
+  const int k = __builtin_amdgcn_frexp_exp(x) >> 1;  // 0, infinity, NaN: 0
+  return ldexpf(rsqrtf((float)ldexp(x, -2 * k)), -k);
+}
+
 // 2^k with the smallest k in [-64, 126] for which amax <= 448 * 2^k; NaN and zero give 2^-64.
 __device__ __forceinline__ float power_scale(double amax) {
   if (!(amax > 0)) return __uint_as_float((127 - 64) << 23);
@@ -74,13 +81,12 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* f) {
 }  // namespace
 
 // A row belongs to LANES lanes of a wave or (LANES = 64) to W waves, which hold E steps of 8 channels a
-// lane. BITS8: the output in 8 bits. There the mean square and the groups' maxima are formed in fp64
-// (h and weight are exact in it, so is their product): the scale steps where a maximum passes 448
-// times a power of two, and must not step by a rounding.
+// lane. BITS8: the output in 8 bits. There the groups' maxima are in fp64 as well (h and weight are exact in
+// it, so is their product): the scale steps where a maximum passes 448 times a power of two, and must not
+// step by a rounding.
 template <typename T, typename TR, int LANES, int E, int W, bool ADD, bool BITS8>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_kernel(ResidualNormArgs a) {
-  typedef typename std::conditional<BITS8, double, float>::type acc;
-  __shared__ acc s_sum[1][W];
+  __shared__ double s_sum[1][W];
   const int lane = threadIdx.x & 63, in_row = lane % LANES;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const long row = W == 1 ? ((long)blockIdx.x * 4 + wave) * (64 / LANES) + lane / LANES : (long)blockIdx.x;
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_kern
     }
   }
   float h[E][8];
-  acc sum[1] = {0};
+  double sum[1] = {0};
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int ch = ((e * W + part) * LANES + in_row) * 8;
@@ -128,12 +134,12 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_kern
       for (int c = 0; c < 8; ++c) h[e][c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) sum[0] += (acc)h[e][c] * (acc)h[e][c];
+    for (int c = 0; c < 8; ++c) sum[0] += (double)h[e][c] * (double)h[e][c];
   }
   row_total<LANES, W>(sum, s_sum, wave);
-  const acc ss = sum[0];
+  const double ms = sum[0] / a.D + (double)a.eps;
   if constexpr (!BITS8) {
-    const float rho = rsqrtf(ss / a.D + a.eps);
+    const float rho = rsqrt_of(ms);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int ch = ((e * W + part) * LANES + in_row) * 8;
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_kern
       }
     }
   } else {
-    const double rho = 1.0 / sqrt(ss / a.D + (double)a.eps);
+    const double rho = 1.0 / sqrt(ms);
     const float rho32 = (float)rho;
     const bool whole = a.group >= a.D;  // one scale a row
     const int lanes = a.group / 8;  // of a group
@@ -201,7 +207,7 @@ template <typename T, typename TR, int LANES, int E, int W, bool DH>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
   constexpr int ROWS = W == 1 ? 4 * (64 / LANES) : 1;  // of a workgroup at a time
   __shared__ __attribute__((aligned(16))) float s_part[ROWS][W == 1 ? E * LANES * 8 : 4];
-  __shared__ float s_sum[2][W];
+  __shared__ double s_sum[2][W];
   const int lane = threadIdx.x & 63, in_row = lane % LANES;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = W == 1 ? 0 : wave;
@@ -218,6 +224,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
     }
   }
   const int mine = W == 1 ? wave * (64 / LANES) + lane / LANES : 0;
+  const double per = 1.0 / a.D;
   for (long row = (long)blockIdx.x * ROWS + mine; row < a.rows; row += (long)gridDim.x * ROWS) {
     Vec8<T> rg[E];
     Vec8<TR> rh[E], rd[E];
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
         rh[e].zero();
       }
     }
-    float sum[2] = {0.f, 0.f};  // h^2, u h
+    double sum[2] = {0, 0};  // h^2, u h
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float g[8], h[8];
@@ -241,14 +248,13 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
       rh[e].to_float(h);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        sum[0] = fmaf(h[c], h[c], sum[0]);
-        sum[1] = fmaf(g[c] * w[e][c], h[c], sum[1]);
+        sum[0] = fma((double)h[c], (double)h[c], sum[0]);
+        sum[1] = fma((double)(g[c] * w[e][c]), (double)h[c], sum[1]);
       }
     }
     row_total<LANES, W>(sum, s_sum, wave);
-    const float ss = sum[0], uh = sum[1];
-    const float rho = rsqrtf(ss / a.D + a.eps);
-    const float back = rho * rho * (uh / a.D);  // rho mean(u n)
+    const float rho = rsqrt_of(fma(sum[0], per, (double)a.eps));
+    const float un = (float)(sum[1] * per * (double)rho);  // mean(u n)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int ch = ((e * W + part) * LANES + in_row) * 8;
@@ -259,8 +265,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) gdn2_residual_norm_bwd_
         if constexpr (DH) rd[e].to_float(d);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float t = rho * (g[c] * w[e][c] - h[c] * back);
-          dw[e][c] = fmaf(g[c], h[c] * rho, dw[e][c]);
+          const float n = h[c] * rho, t = rho * (g[c] * w[e][c] - n * un);
+          dw[e][c] = fmaf(g[c], n, dw[e][c]);
           d[c] = DH ? d[c] + t : t;
         }
         store8((T*)a.dx + row * a.D + ch, d);

@@ -572,7 +572,8 @@ int gdn2_linear_recurrence_tokens(const void* v, const void* log_alpha, const vo
 /*
  * The norm between layers, with the residual's addition:
  *     h = x + residual   (rounded to the residual's type: the stream that the next layer adds to)
- *     y = h / sqrt(mean(h^2) + eps) * weight     (of h as it is stored; fp32 inside)
+ *     y = h / sqrt(mean(h^2) + eps) * weight     (of h as it is stored; fp32 inside,
+ *                                                 sums over a row fp64)
  *
  *   x        : [rows, D] (dtype), row i at element i * x_stride, channels dense
  *   residual : [rows, D] (r_dtype), r_stride likewise; or NULL: h = x, and h is not written
@@ -584,7 +585,8 @@ int gdn2_linear_recurrence_tokens(const void* v, const void* log_alpha, const vo
  *              its group. A row with a NaN or an infinity gives NaN codes where y is NaN.
  *   group    : 0, 32, 64 or 128 channels (0 without scale); D a multiple of it
  *   Supported: D a multiple of 8 up to 16384; types bf16 with bf16, bf16 with an fp32 residual, fp32
- *   with fp32; rows below 2^23. Magnitudes below 2^63, past which the mean square leaves fp32. rows = 0 is a no-op.
+ *   with fp32; rows below 2^23. fp32's precision where sqrt(mean(h^2) + eps) of a row lies between 2^-126
+ *   and 2^126, forward and backward. rows = 0 is a no-op.
  * Returns GDN2_OK or an error status.
  */
 int gdn2_residual_norm(const void* x, const void* residual, const float* weight, void* y, void* h,
