@@ -65,6 +65,23 @@ def _no_second(backward):
     return run
 
 
+def _layout(t):
+    return None if t is None else (t.stride(), t.shape, t.dtype, t.device)
+
+
+def _save(ctx, *tensors):
+    """Saves tensors for the backward pass. What saved-tensor hooks make of them need not have their
+    layout, nor their type; _unpack says whether it has."""
+    ctx.save_for_backward(*tensors)
+    ctx.layouts = [_layout(t) for t in tensors]
+
+
+def _unpack(ctx):
+    """The saved tensors, and whether they lie as those that the forward checked did."""
+    tensors = ctx.saved_tensors
+    return tensors, [_layout(t) for t in tensors] == ctx.layouts
+
+
 # ---------------------------------------------------------------- diagonal recurrence
 
 def _recurrence_args(v, g, w, cu_seqlens):
@@ -100,7 +117,8 @@ def _recurrence_sizes(backward, packed, B, T, D, N):
 
 
 def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
-    B, T, D, N, strides, code, dev, dt = _recurrence_args(v, g, w, cu_seqlens)
+    sizes = _recurrence_args(v, g, w, cu_seqlens)
+    B, T, D, N, strides, code, dev, dt = sizes
     if initial_state is not None:
         _dense("initial_state", initial_state, (N, D), torch.float32, dev)
     o = _empty(v)
@@ -110,7 +128,7 @@ def _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, keep):
     ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
     _call("gdn2_linear_recurrence", dev, v.data_ptr(), g.data_ptr(), _p(w), _p(initial_state),
           o.data_ptr(), _p(last), _p(states), _p(cu_seqlens), B, T, D, N, *strides, code, _p(ws), need)
-    return o, last, states
+    return o, last, states, sizes
 
 
 def linear_recurrence_fwd(v, g, w=None, initial_state=None, cu_seqlens=None,
@@ -133,7 +151,7 @@ def linear_recurrence_fwd_train(v, g, w=None, initial_state=None, cu_seqlens=Non
     """linear_recurrence_fwd for training: (o, final_state, states), the last for
     linear_recurrence_bwd (the fp32 state before every 64th token of every sequence). Rows that belong
     to no packed sequence are zeros."""
-    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)
+    return _recurrence(v, g, w, initial_state, cu_seqlens, output_final_state, True)[:3]
 
 
 def linear_recurrence_bwd(v, g, w, states, do, d_final_state=None, cu_seqlens=None):
@@ -169,19 +187,22 @@ def _recurrence_bwd(v, g, w, states, do, d_final_state, cu_seqlens, sizes):
 class _LinearRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, v, g, w, initial_state, cu_seqlens):
-        o, last, states = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
+        o, last, states, ctx.sizes = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
         ctx.set_materialize_grads(False)
         ctx.has_s0 = initial_state is not None
-        ctx.save_for_backward(v, g, w, states, cu_seqlens)
+        _save(ctx, v, g, w, states, cu_seqlens)
         return o, last
 
     @staticmethod
     @_no_second
     def backward(ctx, do, d_last):
-        v, g, w, states, cu = ctx.saved_tensors  # under hooks other tensors than the forward's: checked again
+        (v, g, w, states, cu), same = _unpack(ctx)
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _aligned_gradient(do)
         d_last = None if d_last is None else _aligned_gradient(d_last)
-        dv, dg, dw, ds0 = linear_recurrence_bwd(v, g, w, states, do, d_last, cu)
+        if same:
+            dv, dg, dw, ds0 = _recurrence_bwd(v, g, w, states, do, d_last, cu, ctx.sizes)
+        else:
+            dv, dg, dw, ds0 = linear_recurrence_bwd(v, g, w, states, do, d_last, cu)
         return dv, dg, dw, ds0 if ctx.has_s0 else None, None
 
 
@@ -348,17 +369,17 @@ class _ResidualNorm(torch.autograd.Function):
         y, _, h = _norm(x, residual, weight, eps, None, None)
         ctx.set_materialize_grads(False)
         ctx.eps = eps
-        ctx.save_for_backward(h, weight)
+        _save(ctx, h, weight)
         ctx.dt = x.dtype
         return y if residual is None else (y, h)
 
     @staticmethod
     @_no_second
     def backward(ctx, dy, dh=None):
-        h, weight = ctx.saved_tensors  # under hooks other tensors than the forward's: checked again
+        (h, weight), same = _unpack(ctx)
         dy = torch.zeros(h.shape, dtype=ctx.dt, device=h.device) if dy is None else _aligned_gradient(dy)
         dh = None if dh is None else _aligned_gradient(dh)
-        dx, dr, dw = residual_norm_bwd(dy, dh, h, weight, ctx.eps)
+        dx, dr, dw = (_norm_bwd if same else residual_norm_bwd)(dy, dh, h, weight, ctx.eps)
         return dx, dr if ctx.needs_input_grad[1] else None, dw, None
 
 
