@@ -7,8 +7,10 @@
 // positive, NaN among them, count as zero.
 //
 // The token is a border in a sum over the vocabulary, so products, differences and sums are in
-// fp64: those of fp32 values are exact or rounded at 2^-53, and no order of a sum moves a border
-// that a draw meets. Bound by HBM where sequences are many (one row of p and one of q are read, 8 V
+// fp64. Those of fp32 values are exact, or rounded at 2^-53 where exponents lie more than 29 bits apart or
+// the row is long: a border is then known to within some 2^-53 of the total, as is u times it, and a draw
+// that near to one may give the neighbouring entry that holds anything. Equal inputs give equal tokens (the
+// orders of the sums are fixed). Bound by HBM where sequences are many (one row of p and one of q are read, 8 V
 // bytes a sequence in fp32: 64 of 131071 entries 12 us, 5.4 TB/s), by the latency of dependent loads
 // where they are few. The first kernel leaves the sums of pieces of kPiece entries, many workgroups a
 // row; the second finds the piece that holds the border and reads that one again (5 us). One

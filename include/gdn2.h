@@ -532,7 +532,9 @@ size_t gdn2_cache_attention_workspace_bytes(int packed, int B, int T, int Hq, in
  *   (With `states`, for training, rows that belong to no packed sequence are written as zeros.)
  *   Supported: D a multiple of 8, both dtypes, B * T below 2^31 - 4096, N * D / 64 below 2^23 (D
  *   rounded up to 64). A NaN or an infinity stays in its own sequence and
- *   channel, from its token on. T = 0 copies the initial state to the final one; N = 0 without `states` is a no-op.
+ *   channel, from its token on. What a decay of less than 2^-126, of one token or of several
+ *   together, leaves of a state may count as nothing. T = 0 copies the initial state to the final one;
+ *   N = 0 without `states` is a no-op.
  * Returns GDN2_OK or an error status.
  */
 int gdn2_linear_recurrence(const void* v, const void* log_alpha, const void* w,
@@ -615,7 +617,8 @@ size_t gdn2_residual_norm_bwd_workspace_bytes(int64_t rows, int D);
  *     draft i is accepted where u_i q_i(x_i) < p_i(x_i) and all before it were;  a: how many were
  *     the next token is drawn from max(p_a - q_a, 0) where draft a was rejected (from p_a where that
  *     is zero everywhere), from p_a where none was: the first j whose cumulated weight passes
- *     u_L times their sum (fp64)
+ *     u_L times their sum (fp64: where the sums are not exact, a draw within some 2^-53 of the
+ *     sum from a border may give the neighbouring entry)
  * Rows need not sum to one. Entries that are not positive count as zero, NaN among them.
  *
  *   target_probs : [N, L + 1, V] (dtype), dense
