@@ -65,23 +65,6 @@ def _no_second(backward):
     return run
 
 
-def _layout(t):
-    return None if t is None else (t.stride(), t.shape, t.dtype, t.device)
-
-
-def _save(ctx, *tensors):
-    """Saves tensors for the backward pass. What saved-tensor hooks make of them need not have their
-    layout, nor their type; _unpack says whether it has."""
-    ctx.save_for_backward(*tensors)
-    ctx.layouts = [_layout(t) for t in tensors]
-
-
-def _unpack(ctx):
-    """The saved tensors, and whether they lie as those that the forward checked did."""
-    tensors = ctx.saved_tensors
-    return tensors, [_layout(t) for t in tensors] == ctx.layouts
-
-
 # ---------------------------------------------------------------- diagonal recurrence
 
 def _recurrence_args(v, g, w, cu_seqlens):
@@ -188,15 +171,29 @@ class _LinearRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, v, g, w, initial_state, cu_seqlens):
         o, last, states, ctx.sizes = _recurrence(v, g, w, initial_state, cu_seqlens, True, True)
+        ctx.kept = states.shape
         ctx.set_materialize_grads(False)
         ctx.has_s0 = initial_state is not None
-        _save(ctx, v, g, w, states, cu_seqlens)
+        ctx.save_for_backward(v, g, w, states, cu_seqlens)
         return o, last
 
     @staticmethod
     @_no_second
     def backward(ctx, do, d_last):
-        (v, g, w, states, cu), same = _unpack(ctx)
+        v, g, w, states, cu = ctx.saved_tensors
+        # Saved-tensor hooks may hand back another layout (slices come back dense), or anything: what does not
+        # lie as the forward's own did goes through the checks from the start.
+        B, T, D, N, strides, code, dev, dt = ctx.sizes
+        shape, index = (B, T, D), dev.index
+        same = (states.shape == ctx.kept and states.dtype is torch.float32 and states.is_contiguous() and
+                states.get_device() == index)
+        for t, step in zip((v, g, w), strides):
+            if t is not None and (t.stride() != (T * step, step, 1) or t.shape != shape or t.dtype is not dt or
+                                  t.get_device() != index):
+                same = False
+        if cu is not None and (cu.shape != (N + 1,) or cu.dtype is not torch.int32 or not cu.is_contiguous() or
+                               cu.get_device() != index):
+            same = False
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _aligned_gradient(do)
         d_last = None if d_last is None else _aligned_gradient(d_last)
         if same:
@@ -369,14 +366,19 @@ class _ResidualNorm(torch.autograd.Function):
         y, _, h = _norm(x, residual, weight, eps, None, None)
         ctx.set_materialize_grads(False)
         ctx.eps = eps
-        _save(ctx, h, weight)
-        ctx.dt = x.dtype
+        ctx.save_for_backward(h, weight)
+        ctx.dt, ctx.ht = x.dtype, h.dtype
         return y if residual is None else (y, h)
 
     @staticmethod
     @_no_second
     def backward(ctx, dy, dh=None):
-        (h, weight), same = _unpack(ctx)
+        h, weight = ctx.saved_tensors
+        # (as for the recurrence: what saved-tensor hooks have changed is checked from the start)
+        out = dh if dy is None else dy  # of the forward's shape and device
+        index = out.device.index
+        same = (h.shape == out.shape and h.dtype is ctx.ht and h.get_device() == index and weight.dtype is torch.float32 and
+                weight.shape == out.shape[-1:] and weight.is_contiguous() and weight.get_device() == index)
         dy = torch.zeros(h.shape, dtype=ctx.dt, device=h.device) if dy is None else _aligned_gradient(dy)
         dh = None if dh is None else _aligned_gradient(dh)
         dx, dr, dw = (_norm_bwd if same else residual_norm_bwd)(dy, dh, h, weight, ctx.eps)
