@@ -8,7 +8,8 @@
 //
 // Bound by HBM: every row is read once and kept in registers between the sum and the output. Sums over a
 // row are in fp64, whose exponent holds the square of any fp32 value and the product of any two; rho and
-// mean(u n) are back in fp32's range where the row's root mean square is.
+// mean(u n) are back in fp32's range where the row's root mean square is. (Against fp32 sums: forward the same
+// times, backward 28.4 -> 29.1 us at 65536 rows of 256, 123 -> 127 at 2048 rows of 16384, else the same.)
 
 #include "gdn2_attn_device.h"
 #include "gdn2_stack_device.h"
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(1024) gdn2_residual_norm_dweight_kernel(const 
 namespace {
 
 // How a row is laid out. Up to 512 channels it takes no more lanes of a wave than it fills (65536 rows
-// of 256: 30 -> 26 us, backward 43 -> 28); wider ones take a wave up to 2048 channels, unless rows are too few to fill the
+// of 256 in bf16: 22-24 us, backward 29; with a wave a row 30 and 43); wider ones take a wave up to 2048 channels, unless rows are too few to fill the
 // card, and 4 or 8 waves above.
 template <int LANES_, int E_, int W_>
 struct Layout {
